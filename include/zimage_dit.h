@@ -361,6 +361,102 @@ ZI_API int zi_attention(const uint16_t* d_qkv, uint16_t* d_out, int batch, int s
 ZI_API int zi_attention_varlen(const uint16_t* d_qkv, uint16_t* d_out, int batch, int seq, int heads,
                                const int32_t* d_kv_len, zi_stream_t stream);
 
+/* ---------------------------------------------------------------- masked attention */
+
+/* One call of zi_attention_masked.  Tensors are bf16 with 128 contiguous elements per
+ * head; q and out [batch, q_len, heads, 128], k and v [batch, kv_len, kv_heads, 128],
+ * each with its own strides (in elements, multiples of 8; the stride of a dimension of
+ * size 1 is not read), so slices of a fused projection, [batch, heads, rows, 128] layouts
+ * and caches with room to grow are passed as they are.  zi_attention_desc_init gives a
+ * desc with every optional field off. */
+typedef struct zi_attention_desc {
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  uint16_t* out;  /* may not overlap the inputs */
+  int64_t q_batch_stride, q_row_stride, q_head_stride;
+  int64_t k_batch_stride, k_row_stride, k_head_stride;
+  int64_t v_batch_stride, v_row_stride, v_head_stride;
+  int64_t out_batch_stride, out_row_stride, out_head_stride;
+  int batch;
+  int heads;     /* query heads, a multiple of kv_heads: head h reads key head h / (heads / kv_heads) */
+  int kv_heads;
+  int q_len;     /* queries per element, 1 .. 2^24 */
+  int kv_len;    /* key rows per element, 1 .. 2^24 */
+  float scale;   /* of q . k; finite, > 0 (1 / sqrt(128) from zi_attention_desc_init) */
+  float softcap; /* scores become softcap * tanh(score / softcap); 0 = no cap; finite, >= 0 */
+  const float* d_slopes;       /* fp32 [heads] or NULL: scores lose slope[h] * |p_i - j|, after the cap */
+  int causal;                  /* 1: query i sees key j only if j <= p_i (or by the prefix); 0: no order */
+  const int32_t* d_prefix_len; /* int32 [batch] or NULL (needs causal): keys j < prefix[b] are seen by every query */
+  const int32_t* d_kv_len;     /* int32 [batch] or NULL: keys of each element, clamped to [0, kv_len] on the device */
+  const int32_t* d_q_doc;      /* int32 [batch, q_len] and ... */
+  const int32_t* d_k_doc;      /* ... [batch, kv_len] document ids, both or NULL: a query sees the keys of its own
+                                  id, in any order; a negative id sees nothing and is seen by nothing */
+} zi_attention_desc;
+
+/* Fill *desc with NULL pointers, zero sizes and strides, scale 1 / sqrt(128) and no masks.
+ * ZI_ERR_ARG if desc is NULL. */
+ZI_API int zi_attention_desc_init(zi_attention_desc* desc);
+
+/* Attention with capped scores, a bias that falls with distance, and masks:
+ *   s_ij = scale q_i . k_j;  s = softcap tanh(s / softcap);  s -= slope[h] |p_i - j|;
+ *   out_i = sum_j softmax_j(s_ij) v_j   over the keys that query i sees.
+ * An element's queries are the last of its n keys (n = kv_len or d_kv_len[b]): query i
+ * stands at p_i = i + n - q_len, so q_len = 1 is one step over a cache and q_len = n self
+ * attention.  The masks given apply together.  A query that sees no key (no keys, all
+ * masked, a negative id) gets zeros.  fp32 scores and softmax, probabilities rounded to
+ * bf16 for the second product, one rounding of the result.
+ * What key rows past an element's end and rows with a negative id hold is never used (NaN
+ * included).  A key that some queries see has to be finite: the product of a masked
+ * probability (zero) and a NaN or infinity in a seen row of v is NaN.
+ * No workspace, nothing kept between calls: any number of calls may run at once. */
+ZI_API int zi_attention_masked(const zi_attention_desc* desc, zi_stream_t stream);
+
+/* ---------------------------------------------------------------- 4-bit rows and their product */
+
+/* Microscaled 4-bit formats: e2m1 elements (0, 0.5, 1, 1.5, 2, 3, 4, 6 and negatives), two
+ * to a byte, the even column in the low half, under block scales. */
+enum zi_fp4_format {
+  ZI_FP4_MX = 0, /* MXFP4 (OCP microscaling): 32 columns share the scale 2^(c - 127), stored as the byte c */
+  ZI_FP4_NV = 1  /* NVFP4: 16 columns share an e4m3 scale, and each row has an fp32 scale */
+};
+
+/* Bytes of the block scales of a [rows, cols] matrix.  They are stored as the tensor core
+ * takes them: tiles of 128 rows x 4 blocks, 512 bytes each, tiles row-major; row i, block j
+ * of a tile is byte (i % 32) * 16 + (i / 32) * 4 + j, and blocks outside the matrix hold 0. */
+ZI_API int zi_fp4_scale_size(int format, int rows, int cols, size_t* h_bytes);
+
+/* Rows to 4 bits, each value to the nearest (ties to the even code), saturating at 6:
+ *   MXFP4  X = 2^(floor(log2 amax) - 2) of 32 columns (at least 2^-127; 1 if all are zero)
+ *          and e2m1(x / X): the OCP conversion
+ *   NVFP4  r = the smallest power of two with amax_row <= 448 * 6 * r (at least 2^-126; 1 for
+ *          a row of zeros), S = e4m3(amax / (6 r)) of 16 columns, and e2m1(x / (S r))
+ * with the results of exact arithmetic, whatever the input's type.  A block that holds an
+ * infinity or a NaN gets the NaN scale and zero codes (NVFP4: r is taken from the others).
+ *   d_x   [rows, cols] fp32 (x_bf16 = 0) or bf16 (x_bf16 = 1), contiguous
+ *   d_q   [rows, cols / 2] codes;  d_bs zi_fp4_scale_size() bytes of block scales
+ *   d_rs  [rows] fp32 row scales r (NVFP4; NULL for MXFP4)
+ * cols % 32 == 0, cols <= 16384, rows <= 2^30 (ZI_ERR_SHAPE); 16-byte aligned pointers.
+ * rows == 0 enqueues nothing. */
+ZI_API int zi_quantize_fp4(int format, const void* d_x, int x_bf16, int rows, int cols, uint8_t* d_q, uint8_t* d_bs,
+                           float* d_rs, zi_stream_t stream);
+
+/* The values that such a matrix stands for, code * block scale * row scale: bf16 (y_bf16 =
+ * 1) or fp32, [rows, cols] contiguous.  Exact for what zi_quantize_fp4 stores, down to the
+ * output type's smallest normal number.  Restrictions as for zi_quantize_fp4. */
+ZI_API int zi_dequantize_fp4(int format, const uint8_t* d_q, const uint8_t* d_bs, const float* d_rs, int rows,
+                             int cols, void* d_y, int y_bf16, zi_stream_t stream);
+
+/* C[M, N] = bf16( ra[m] rb[n] sum_k A[m, k] B[n, k] ), A and B 4-bit matrices of one format
+ * (codes, block scales, and row scales for NVFP4; NULL row scales for MXFP4), on the
+ * tensor cores (kind::mxf4nvf4), fp32 accumulate, one rounding.  A row that holds a NaN
+ * scale gives a row (of A) or column (of B) of NaN.
+ * K % 32 == 0, N % 8 == 0, M >= 0 (0 enqueues nothing), each at most 2^24 (ZI_ERR_SHAPE); 16-byte
+ * aligned pointers.  No workspace, nothing kept between calls. */
+ZI_API int zi_gemm_fp4(int format, const uint8_t* d_a, const uint8_t* d_abs, const float* d_ars, const uint8_t* d_b,
+                       const uint8_t* d_bbs, const float* d_brs, uint16_t* d_c, int m, int n, int k,
+                       zi_stream_t stream);
+
 /* Test hook for the attention softmax's second exponential: d_y[i] = 2^d_x[i] as the
  * attention kernel computes it on the FMA pipe for 3 of every 8 score pairs (the rest
  * go to the MUFU ex2 unit), so that its accuracy can be checked directly.  The method
@@ -399,7 +495,11 @@ enum zi_kernel_kind {
   ZI_KERNEL_SPLIT_CLEAR = 18,   /* zero the GEMM split-tail counters (once per forward) */
   ZI_KERNEL_QUANTIZE = 19,      /* zi_quantize_rows_e4m3 */
   ZI_KERNEL_SELFTEST = 20,      /* zi_watchdog_selftest */
-  ZI_KERNEL_EXP2_TEST = 21      /* zi_exp2_poly */
+  ZI_KERNEL_EXP2_TEST = 21,     /* zi_exp2_poly */
+  ZI_KERNEL_QUANTIZE_FP4 = 22,  /* zi_quantize_fp4 */
+  ZI_KERNEL_DEQUANTIZE_FP4 = 23, /* zi_dequantize_fp4 */
+  ZI_KERNEL_GEMM_FP4 = 24,      /* zi_gemm_fp4 */
+  ZI_KERNEL_ATTENTION_MASKED = 25 /* zi_attention_masked */
 };
 
 /* Start recording launch timings on this host thread: from the next kernel the

@@ -8,13 +8,14 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_char_p, c_double, c_float, c_int, c_size_t, c_void_p
+from ctypes import POINTER, c_char_p, c_double, c_float, c_int, c_int64, c_size_t, c_void_p
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libzimage_dit.so")
 
 ZI_OK, ZI_ERR_ARG, ZI_ERR_SHAPE, ZI_ERR_ALIGN, ZI_ERR_WORKSPACE, ZI_ERR_CUDA, ZI_ERR_TIMEOUT, ZI_ERR_DEVICE = (
     0, -1, -2, -3, -4, -5, -6, -7)
 ZI_ERR_SCRATCH_LIMIT = -8
+ZI_FP4_MX, ZI_FP4_NV = 0, 1
 STATIC_SCRATCH_BYTES = 128 * 1024 * 1024
 
 
@@ -51,6 +52,14 @@ class ZiModelWeights(ctypes.Structure):
         ("cap_pad", c_void_p)]
 
 
+class ZiAttentionDesc(ctypes.Structure):
+    _fields_ = [(n, c_void_p) for n in ("q", "k", "v", "out")] + [
+        (f"{t}_{d}_stride", c_int64) for t in ("q", "k", "v", "out") for d in ("batch", "row", "head")] + [
+        (n, c_int) for n in ("batch", "heads", "kv_heads", "q_len", "kv_len")] + [
+        ("scale", c_float), ("softcap", c_float), ("d_slopes", c_void_p), ("causal", c_int),
+        ("d_prefix_len", c_void_p), ("d_kv_len", c_void_p), ("d_q_doc", c_void_p), ("d_k_doc", c_void_p)]
+
+
 _SIGS = {
     "zi_status_string": (c_char_p, [c_int]),
     "zi_version": (c_int, []),
@@ -83,6 +92,13 @@ _SIGS = {
     "zi_quantize_rows_e4m3": (c_int, [c_void_p, c_int, c_int, c_int, c_void_p, c_void_p, c_void_p]),
     "zi_gemm_e4m3": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_void_p]),
     "zi_attention_varlen": (c_int, [c_void_p, c_void_p, c_int, c_int, c_int, c_void_p, c_void_p]),
+    "zi_attention_desc_init": (c_int, [POINTER(ZiAttentionDesc)]),
+    "zi_attention_masked": (c_int, [POINTER(ZiAttentionDesc), c_void_p]),
+    "zi_fp4_scale_size": (c_int, [c_int, c_int, c_int, POINTER(c_size_t)]),
+    "zi_quantize_fp4": (c_int, [c_int, c_void_p, c_int, c_int, c_int, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "zi_dequantize_fp4": (c_int, [c_int, c_void_p, c_void_p, c_void_p, c_int, c_int, c_void_p, c_int, c_void_p]),
+    "zi_gemm_fp4": (c_int, [c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int,
+                            c_int, c_int, c_void_p]),
     "zi_profile_begin": (c_int, [c_int]),
     "zi_profile_end": (c_int, [POINTER(c_float), POINTER(c_int), c_int, POINTER(c_int)]),
     "zi_watchdog_selftest": (c_int, [c_int, c_void_p]),
@@ -146,6 +162,18 @@ def model_workspace_size(cfg: ZiConfig, batch: int, lat_h: int, lat_w: int, s_tx
     return n.value
 
 
+def fp4_scale_size(fmt: int, rows: int, cols: int) -> int:
+    n = c_size_t(0)
+    call("zi_fp4_scale_size", fmt, rows, cols, ctypes.byref(n))
+    return n.value
+
+
+def attention_desc_init() -> ZiAttentionDesc:
+    d = ZiAttentionDesc()
+    call("zi_attention_desc_init", ctypes.byref(d))
+    return d
+
+
 def sigmas(n_steps: int, shift: float = 3.0):
     out = (c_double * (n_steps + 1))()
     call("zi_sigmas", n_steps, shift, out)
@@ -177,7 +205,7 @@ KERNEL_NAMES = {
     5: "gemm_ffn_down", 6: "post_norm_residual", 7: "pre_norm", 8: "adaln_gemv", 9: "timestep_mlp",
     10: "rope_table", 11: "positions", 12: "patchify", 13: "gemm_embed", 14: "gemm_final_unpatchify",
     15: "euler", 16: "gemm", 17: "text_pad", 18: "split_clear", 19: "quantize_e4m3", 20: "watchdog_selftest",
-    21: "exp2_poly_test",
+    21: "exp2_poly_test", 22: "quantize_fp4", 23: "dequantize_fp4", 24: "gemm_fp4", 25: "attention_masked",
 }
 
 

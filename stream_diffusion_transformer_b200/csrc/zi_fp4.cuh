@@ -1,0 +1,552 @@
+// Microscaled 4-bit floating point: rows of e2m1 values under block scales, and their
+// product on the tensor cores (tcgen05.mma kind::mxf4nvf4, fp32 accumulate).
+//
+// Formats.  Elements are e2m1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives, packed
+// two to a byte with the even column in the low half.
+//   MXFP4  blocks of 32 columns, scale 2^(c - 127) stored as the byte c (e8m0)
+//   NVFP4  blocks of 16 columns, scale an e4m3 byte, and one fp32 scale per row
+// Block scales are stored as the tensor core takes them: tiles of 128 rows x 4 blocks,
+// 512 bytes each, tiles row-major; row i, block j of a tile is byte
+// (i % 32) * 16 + (i / 32) * 4 + j.  Blocks outside the matrix hold zero.
+#pragma once
+#include <cuda_fp4.h>
+
+#include "zi_common.cuh"
+
+namespace zi {
+namespace fp4 {
+
+enum : int { MX = 0, NV = 1 };
+
+template <int FMT>
+constexpr int kBlock = FMT == MX ? 32 : 16;
+
+constexpr int kTileBytes = 512;  // one scale tile: 128 rows x 4 blocks
+
+// Scale tiles along a row of `cols` columns / down `rows` rows.
+template <int FMT>
+__host__ __device__ constexpr int tiles_along(int cols) {
+  return (cols + 4 * kBlock<FMT> - 1) / (4 * kBlock<FMT>);
+}
+__host__ __device__ constexpr int tiles_down(int rows) { return (rows + 127) / 128; }
+
+// Offset of the 4-byte word that holds the scales of `row`'s blocks 4 tile .. 4 tile + 3.
+ZI_DEV size_t scale_word(int row, int tile, int tiles_x) {
+  return (size_t(row >> 7) * tiles_x + tile) * kTileBytes + (row & 31) * 16 + ((row >> 5) & 3) * 4;
+}
+
+// ------------------------------------------------------------------ rows
+
+constexpr int kRowsThreads = 256;
+
+// 16 consecutive elements of a row as fp32, and the largest |x| as its bit pattern (an
+// integer maximum, so that infinities and NaN come out on top instead of being dropped).
+struct Span16 {
+  float v[16];
+  uint32_t amax;
+};
+
+ZI_DEV Span16 load_span(const float* p) {
+  Span16 s;
+  s.amax = 0;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint4 w = __ldg(reinterpret_cast<const uint4*>(p) + q);
+    const uint32_t b[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s.v[4 * q + i] = __uint_as_float(b[i]);
+      s.amax = max(s.amax, b[i] & 0x7FFFFFFFu);
+    }
+  }
+  return s;
+}
+
+ZI_DEV Span16 load_span(const uint16_t* p) {
+  Span16 s;
+  s.amax = 0;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const uint4 w = __ldg(reinterpret_cast<const uint4*>(p) + q);
+    const uint32_t b[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = b[i] << 16, hi = b[i] & 0xFFFF0000u;
+      s.v[8 * q + 2 * i] = __uint_as_float(lo);
+      s.v[8 * q + 2 * i + 1] = __uint_as_float(hi);
+      s.amax = max(s.amax, max(lo & 0x7FFFFFFFu, hi & 0x7FFFFFFFu));
+    }
+  }
+  return s;
+}
+
+constexpr uint32_t kInfBits = 0x7F800000u;
+
+// e8m0 byte of an MXFP4 block: floor(log2 amax) - 2 (6 = 1.5 * 2^2 is the largest
+// element), at least -127; a block of zeros gets scale 1, one with an infinity or a NaN
+// the NaN scale.
+ZI_DEV uint32_t mx_scale(uint32_t amax) {
+  if (amax >= kInfBits) return 0xFFu;
+  if (amax == 0) return 127u;
+  const uint32_t e = amax >> 23;  // floor(log2 amax) + 127, or 0 below the normal numbers
+  return e < 2 ? 0u : e - 2;
+}
+
+// Row scale of NVFP4 as a biased exponent: the smallest power of two r with amax <= 448 *
+// 6 * r (2688 = 1.3125 * 2^11), at least 2^-126; a row of zeros gets r = 1.  With a power
+// of two every later product by r is exact, so the codes are those of exact arithmetic.
+ZI_DEV uint32_t nv_row_exp(uint32_t amax) {
+  if (amax == 0) return 127u;
+  const int e = int(amax >> 23) - 11 + ((amax & 0x7FFFFFu) > 0x280000u ? 1 : 0);
+  return e < 1 ? 1u : uint32_t(e);
+}
+
+ZI_DEV float exp_float(uint32_t biased) { return __uint_as_float(biased << 23); }
+
+// q is the quotient of a by b rounded to fp32.  The borders between two e4m3 (or e2m1)
+// values have at most five significant bits; when q falls on such a number the exact
+// quotient may lie on either side of it, and the sign of a - q b (exact) moves q one step
+// that way, so that rounding q decides as rounding the exact quotient would.
+ZI_DEV float off_border(float q, float a, float b) {
+  const uint32_t u = __float_as_uint(q);
+  if ((u & 0x7FFFFu) == 0u) {
+    const float rem = fmaf(-q, b, a);
+    if (rem != 0.f && q != 0.f) return __uint_as_float((rem > 0.f) == (q > 0.f) ? u + 1 : u - 1);
+  }
+  return q;
+}
+
+// e4m3 byte of an NVFP4 block: amax / (6 r), rounded to nearest even.
+ZI_DEV uint32_t nv_scale(uint32_t amax, uint32_t row_exp) {
+  if (amax >= kInfBits) return 0x7Fu;
+  const float t = __uint_as_float(amax) * exp_float(254u - row_exp);  // amax / r, exact
+  const float q = off_border(__fdiv_rn(t, 6.f), t, 6.f);
+  return __nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
+}
+
+ZI_DEV float e4m3_float(uint32_t byte) {
+  const __half_raw h = __nv_cvt_fp8_to_halfraw(__nv_fp8_storage_t(byte), __NV_E4M3);
+  return __half2float(__half(h));
+}
+
+// 16 e2m1 codes (8 bytes, in column order) of v[i] = x[i] / scale, to nearest even,
+// saturating at 6.
+ZI_DEV uint2 codes16(const float* v) {
+  uint32_t w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    w[h] = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t b = __nv_cvt_float2_to_fp4x2(make_float2(v[8 * h + 2 * i], v[8 * h + 2 * i + 1]), __NV_E2M1,
+                                                  cudaRoundNearest);
+      w[h] |= b << (8 * i);
+    }
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// Rows of x [rows, cols] to codes, block scales and (NVFP4) row scales.  One thread per 16
+// columns, `tpr` threads (a power of two, up to the whole CTA) per row, NB spans per thread
+// for rows wider than 16 tpr.  x is read once; an NVFP4 row waits in registers for its
+// maximum.  Rows past the end up to the scale tile's 128 only write their zero scales.
+template <int FMT, typename TIn, int NB>
+__global__ void __launch_bounds__(kRowsThreads) quantize_kernel(const TIn* __restrict__ x, int rows, int cols, int tpr,
+                                                               uint8_t* __restrict__ q, uint8_t* __restrict__ bs,
+                                                               float* __restrict__ rs) {
+  __shared__ uint32_t red[kRowsThreads / 32];
+  const int sub = threadIdx.x & (tpr - 1);
+  const int row = int(blockIdx.x * (kRowsThreads / tpr) + threadIdx.x / tpr);
+  const int spans = cols / 16;
+  const int tiles_x = tiles_along<FMT>(cols);
+  const int rows_pad = tiles_down(rows) * 128;
+
+  Span16 s[NB];
+  uint32_t am = 0;
+#pragma unroll
+  for (int k = 0; k < NB; ++k) {
+    const int i = sub + k * tpr;
+    s[k].amax = 0;
+    if (row < rows && i < spans) {
+      s[k] = load_span(x + size_t(row) * cols + size_t(i) * 16);
+      if (FMT == NV && s[k].amax < kInfBits) am = max(am, s[k].amax);
+    }
+  }
+  uint32_t row_exp = 127u;
+  if constexpr (FMT == NV) {
+    for (int o = (tpr < 32 ? tpr : 32) >> 1; o > 0; o >>= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
+    if (tpr > 32) {  // the row spans warps
+      if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = am;
+      __syncthreads();
+      const int w0 = (threadIdx.x / tpr) * (tpr / 32);
+      for (int w = 0; w < tpr / 32; ++w) am = max(am, red[w0 + w]);
+    }
+    row_exp = nv_row_exp(am);
+    if (sub == 0 && row < rows) rs[row] = exp_float(row_exp);
+  }
+#pragma unroll
+  for (int k = 0; k < NB; ++k) {
+    const int i = sub + k * tpr;
+    const bool have = row < rows && i < spans;
+    uint32_t byte = 0;
+    if constexpr (FMT == MX) {
+      const uint32_t both = max(s[k].amax, __shfl_xor_sync(0xffffffffu, s[k].amax, 1));
+      if (have) {
+        byte = mx_scale(both);
+        if (both < kInfBits) {
+          const float inv = exp_float(254u - byte);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) s[k].v[e] *= inv;  // exact (a power of two), or far below half a step
+        }
+      }
+      if (both >= kInfBits) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[k].v[e] = 0.f;
+      }
+    } else {
+      if (have) {
+        byte = nv_scale(s[k].amax, row_exp);
+        const float sc = e4m3_float(byte);
+        if (byte == 0u || byte == 0x7Fu) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) s[k].v[e] = byte ? 0.f : copysignf(0.f, s[k].v[e]);
+        } else {
+          const float rinv = exp_float(254u - row_exp), inv = __frcp_rn(sc);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float xr = s[k].v[e] * rinv;  // exact, or far below half a step
+            const float v0 = xr * inv;
+            const float v1 = fmaf(fmaf(-v0, sc, xr), inv, v0);  // one Newton step on the residual
+            // a bf16 x has 8 bits: its quotient hits a border exactly or lies far from it.  The sign of a zero is kept.
+            s[k].v[e] = copysignf(sizeof(TIn) == 4 ? off_border(v1, xr, sc) : v1, xr);
+          }
+        }
+      }
+    }
+    if (have) *reinterpret_cast<uint2*>(q + size_t(row) * (cols / 2) + size_t(i) * 8) = codes16(s[k].v);
+    // four block scales to a word
+    constexpr int kStep = kBlock<FMT> / 16;  // threads per block
+    uint32_t word = byte;
+#pragma unroll
+    for (int j = 1; j < 4; ++j) word |= __shfl_down_sync(0xffffffffu, byte, j * kStep) << (8 * j);
+    const int tile = i / (4 * kStep);
+    if ((i & (4 * kStep - 1)) == 0 && tile < tiles_x && row < rows_pad)
+      *reinterpret_cast<uint32_t*>(bs + scale_word(row, tile, tiles_x)) = word;
+  }
+}
+
+// The values that codes and scales stand for, bf16 or fp32: one thread per 16 columns.
+template <int FMT, typename TOut>
+__global__ void __launch_bounds__(kRowsThreads) dequantize_kernel(const uint8_t* __restrict__ q,
+                                                                 const uint8_t* __restrict__ bs,
+                                                                 const float* __restrict__ rs, int rows, int cols,
+                                                                 TOut* __restrict__ y) {
+  const int spans = cols / 16;
+  const size_t t = size_t(blockIdx.x) * kRowsThreads + threadIdx.x;
+  if (t >= size_t(rows) * spans) return;
+  const int row = int(t / spans), i = int(t % spans);
+  const int block = i * 16 / kBlock<FMT>;
+  const uint32_t byte = bs[scale_word(row, block >> 2, tiles_along<FMT>(cols)) + (block & 3)];
+  float lo = 1.f, hi;  // value = code * lo * hi, the last product the only one that may round (below the normal numbers)
+  if constexpr (FMT == MX) {
+    // 2^(c - 127) in two factors: c = 0 lies below the normal numbers, c = 255 is NaN
+    hi = byte == 0xFFu ? __uint_as_float(0x7FC00000u) : exp_float(byte == 0 ? 1u : byte);
+    lo = byte == 0 ? 0.5f : 1.f;
+  } else {
+    lo = e4m3_float(byte);
+    hi = rs[row];
+  }
+  const uint2 w = *reinterpret_cast<const uint2*>(q + t * 8);
+  const uint32_t ww[2] = {w.x, w.y};
+  float v[16];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const __half2_raw r = __nv_cvt_fp4x2_to_halfraw2(__nv_fp4x2_storage_t((ww[h] >> (8 * b)) & 0xFFu), __NV_E2M1);
+      const float2 f = __half22float2(__half2(r));
+      v[8 * h + 2 * b] = f.x * lo * hi;
+      v[8 * h + 2 * b + 1] = f.y * lo * hi;
+    }
+  if constexpr (sizeof(TOut) == 4) {
+    float4* d = reinterpret_cast<float4*>(y + t * 16);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) d[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+  } else {
+    uint4* d = reinterpret_cast<uint4*>(y + t * 16);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      d[k] = make_uint4(pack_bf16x2(v[8 * k], v[8 * k + 1]), pack_bf16x2(v[8 * k + 2], v[8 * k + 3]),
+                        pack_bf16x2(v[8 * k + 4], v[8 * k + 5]), pack_bf16x2(v[8 * k + 6], v[8 * k + 7]));
+  }
+}
+
+// ------------------------------------------------------------------ product: shared parts
+
+// D[tmem] (+)= (A * SA)(B * SB)^T for 64 columns of K, both operands e2m1 in smem, block
+// scales in TMEM (one byte per row and block; MXFP4 2 blocks, NVFP4 4 blocks per instruction).
+template <int FMT>
+ZI_DEV void mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sa_tmem, uint32_t sb_tmem,
+                uint32_t accumulate) {
+  if constexpr (FMT == MX) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sa_tmem), "r"(sb_tmem)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sa_tmem), "r"(sb_tmem)
+        : "memory");
+  }
+}
+
+// Instruction descriptor: e2m1 A and B (format code 1), K-major, block scales e8m0 or e4m3.
+// `pair`: which half of the 4-byte scale word an MXFP4 instruction takes (0 or 1).
+template <int FMT>
+__host__ __device__ constexpr uint32_t idesc(int M, int N, int pair) {
+  return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | ((FMT == MX ? 1u : 0u) << 23) |
+         (static_cast<uint32_t>(M >> 7) << 27) | (static_cast<uint32_t>(2 * pair) << 4) |
+         (static_cast<uint32_t>(2 * pair) << 29);
+}
+
+// Descriptor of one 512-byte scale tile in smem for tcgen05.cp 32x128b: 32 rows of 16 bytes,
+// no swizzle, 8-row groups 128 bytes apart.
+ZI_DEV uint64_t scale_desc(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(128u >> 4) << 32;
+  d |= 1ull << 46;
+  return d;
+}
+
+// One scale tile to 4 TMEM columns (column c: rows 32 c .. 32 c + 31 on the lanes, repeated
+// in every lane quarter).  Runs in order with the MMAs issued by the same thread.
+ZI_DEV void copy_scales(uint32_t tmem_col, uint32_t saddr) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem_col), "l"(scale_desc(saddr)) : "memory");
+}
+
+// Untiled bulk copy into this CTA's smem, completing on `bar`.
+ZI_DEV void bulk_load(void* smem_dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(smem_dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+constexpr int kStageK = 256;  // columns of K per stage: 128 bytes of codes per row
+template <int FMT>
+constexpr int kStageTiles = kStageK / (4 * kBlock<FMT>);  // scale tiles per stage and 128 rows: 2 or 4
+
+struct GemmParams {
+  const uint8_t* abs;  // block scales of A [M, K] ...
+  const uint8_t* bbs;  // ... and of B [N, K]
+  const float* ars;    // row scales (NVFP4) [M], or null
+  const float* brs;    // [N], or null
+  uint16_t* out;       // bf16 [M, N]
+  int M, N, K;
+};
+
+// ------------------------------------------------------------------ product: few rows
+// One CTA per 128 rows of B (output columns) x TN rows of A, with B as the instruction's
+// M operand: a call with few rows is bound by reading B, so B's rows fill the tensor core
+// and A's few rows are its N.  A cluster of CTAs shares a tile's K: each takes a run of
+// stages, leaves its fp32 partial in its own smem, and sums a part of the tile over the
+// cluster's CTAs in rank order.  Warps: 0 loads, 1 MMA, 2..5 epilogue.
+constexpr int kNarrowThreads = 192;
+
+template <int FMT, int TN>
+struct NarrowSmem {
+  static constexpr uint32_t kB = 128 * 128;                       // B: 128 rows x 128 bytes
+  static constexpr uint32_t kA = TN * 128 < 1024 ? 1024 : TN * 128;
+  static constexpr uint32_t kSc = kStageTiles<FMT> * kTileBytes;  // scales of one operand
+  static constexpr uint32_t kStage = kB + kA + 2 * kSc;
+  static constexpr int kStages = TN <= 32 ? 4 : 5;
+  static constexpr uint32_t kBar = kStages * kStage;
+  static constexpr uint32_t kBytes = kBar + 256 + 1024;
+  static constexpr uint32_t kCols = TN <= 32 ? 128 : 256;         // TMEM: D, then two scale buffers
+  static constexpr uint32_t kColScale = TN < 32 ? 32 : TN;
+  static constexpr uint32_t kScaleCols = 2 * 4 * kStageTiles<FMT>;  // B's and A's, per buffer
+  static_assert(kColScale + 2 * kScaleCols <= kCols, "TMEM columns");
+  static_assert(kStage % 1024 == 0 && 128 * TN * 4 <= kBar, "stage alignment; the partial fits the ring");
+};
+
+template <int FMT, int TN>
+__global__ void __launch_bounds__(kNarrowThreads)
+    gemm_narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, GemmParams p,
+                       int splits) {
+  using L = NarrowSmem<FMT, TN>;
+  constexpr int kStages = L::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar);
+  uint64_t* empty = full + kStages;
+  uint64_t* done = empty + kStages;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = int(blockIdx.x) % splits;
+  const int n0 = int(blockIdx.x) / splits * 128, m0 = int(blockIdx.y) * TN;
+  const int stages = (p.K + kStageK - 1) / kStageK;
+  const int k0 = int(static_cast<long long>(rank) * stages / splits);
+  const int k1 = int(static_cast<long long>(rank + 1) * stages / splits);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(done, 1);
+    *abort_flag = device_error_set() ? 1 : 0;  // an earlier kernel timed out: leave everything untouched
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmB);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, L::kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const bool skip = *abort_flag != 0;
+  const int tiles_x = tiles_along<FMT>(p.K);
+  const int nk = k1 - k0;
+
+  if (!skip && warp == 0) {
+    if (lane == 0) {
+      int it = 0;
+      bool ok = true;
+      for (; it < nk; ++it) {
+        const int s = it % kStages;
+        if (!mbar_wait(&empty[s], ((it / kStages) & 1) ^ 1, abort_flag, ZI_DEVERR_TIMEOUT_PRODUCER)) {
+          ok = false;
+          break;
+        }
+        const int kb = k0 + it;
+        const int t0 = kb * kStageTiles<FMT>;
+        const uint32_t sc = uint32_t(min(kStageTiles<FMT>, tiles_x - t0)) * kTileBytes;
+        uint8_t* sb = smem + s * L::kStage;
+        mbar_arrive_expect_tx(&full[s], L::kB + TN * 128 + 2 * sc);
+        tma_load_2d(sb, &tmB, &full[s], kb * 128, n0);
+        tma_load_2d(sb + L::kB, &tmA, &full[s], kb * 128, m0);
+        bulk_load(sb + L::kB + L::kA, p.bbs + (size_t(n0 >> 7) * tiles_x + t0) * kTileBytes, sc, &full[s]);
+        bulk_load(sb + L::kB + L::kA + L::kSc, p.abs + (size_t(m0 >> 7) * tiles_x + t0) * kTileBytes, sc, &full[s]);
+      }
+      if (!ok) {  // let the copies already issued land
+        volatile int never = 0;
+        for (int j = it > kStages ? it - kStages : 0; j < it; ++j)
+          mbar_wait(&full[j % kStages], (j / kStages) & 1, &never, ZI_DEVERR_TIMEOUT_DRAIN);
+      }
+    }
+  } else if (!skip && warp == 1) {
+    if (lane == 0) {
+      for (int it = 0; it < nk; ++it) {
+        const int s = it % kStages;
+        if (!mbar_wait(&full[s], (it / kStages) & 1, abort_flag, ZI_DEVERR_TIMEOUT_MMA)) break;
+        tc_fence_after();
+        const uint32_t b_addr = smem_u32(smem + s * L::kStage), a_addr = b_addr + L::kB, sc_addr = a_addr + L::kA;
+        const uint32_t tsb = tmem + L::kColScale + (it & 1) * L::kScaleCols, tsa = tsb + 4 * kStageTiles<FMT>;
+        const int kleft = p.K - (k0 + it) * kStageK;
+        const int ksteps = kleft >= kStageK ? 4 : (kleft + 63) / 64;
+        const int tiles = min(kStageTiles<FMT>, tiles_x - (k0 + it) * kStageTiles<FMT>);
+        for (int t = 0; t < tiles; ++t) {
+          copy_scales(tsb + 4 * t, sc_addr + t * kTileBytes);
+          copy_scales(tsa + 4 * t, sc_addr + L::kSc + t * kTileBytes);
+        }
+        const uint32_t a_col = uint32_t(m0 & 127) / 32;  // the tile's rows inside its 128-row scale tile
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (k < ksteps) {
+            const int t = FMT == MX ? k >> 1 : k;
+            mma<FMT>(tmem, smem_desc_sw128(b_addr + k * 32, 16), smem_desc_sw128(a_addr + k * 32, 16),
+                     idesc<FMT>(128, TN, FMT == MX ? k & 1 : 0), tsb + 4 * t, tsa + 4 * t + a_col,
+                     (it | k) != 0 ? 1u : 0u);
+          }
+        }
+        tc_commit(&empty[s]);
+      }
+      tc_commit(done);  // after an abort too: TMEM and smem are reused once every MMA issued has finished
+      volatile int never = 0;
+      mbar_wait(done, 0, &never, ZI_DEVERR_TIMEOUT_DRAIN);
+    }
+  }
+  // the partial, column-major: [TN][128] fp32 over the ring (every copy has landed, every MMA is done)
+  __syncthreads();
+  tc_fence_after();
+  float* part = reinterpret_cast<float*>(smem);
+  const int q = warp & 3;
+  if (warp >= 2 && !*abort_flag) {
+#pragma unroll 1
+    for (int c = 0; c < TN; c += 16) {
+      uint32_t v[16];
+      asm volatile(
+          "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+          "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+          : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+            "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+          : "r"(tmem + (uint32_t(q * 32) << 16) + c));
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        asm volatile("" : "+r"(v[i]));
+        part[(c + i) * 128 + q * 32 + lane] = nk > 0 ? __uint_as_float(v[i]) : 0.f;
+      }
+    }
+  }
+  if (splits > 1) cluster_sync(); else __syncthreads();
+  // this CTA's share of the tile's TN columns, summed over the ranks in order
+  const int c0 = rank * TN / splits, c1 = (rank + 1) * TN / splits;
+  bool bad = *abort_flag != 0;
+  const uint32_t base = smem_u32(part), flag = smem_u32(const_cast<int*>(abort_flag));
+  if (splits > 1) {
+    for (int r = 0; r < splits; ++r) {
+      uint32_t addr, f;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(flag), "r"(r));
+      asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(f) : "r"(addr) : "memory");
+      bad = bad || f != 0;
+    }
+  }
+  const int pair = int(threadIdx.x) & 63;  // two neighbouring output columns
+  const int n = n0 + 2 * pair;
+  if (!bad && n < p.N) {  // N is even
+    const float s0 = p.brs ? __ldg(p.brs + n) : 1.f, s1 = p.brs ? __ldg(p.brs + n + 1) : 1.f;
+    for (int c = c0 + int(threadIdx.x >> 6); c < c1; c += kNarrowThreads / 64) {
+      const int m = m0 + c;
+      if (m >= p.M) break;
+      float x = 0.f, y = 0.f;
+      for (int r = 0; r < splits; ++r) {
+        float u, w;
+        uint32_t addr = base + uint32_t(c * 128 + 2 * pair) * 4;
+        if (splits > 1) {
+          asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(addr), "r"(r));
+          asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(u), "=f"(w) : "r"(addr) : "memory");
+        } else {
+          asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(u), "=f"(w) : "r"(addr) : "memory");
+        }
+        x += u;
+        y += w;
+      }
+      const float a = p.ars ? __ldg(p.ars + m) : 1.f;
+      *reinterpret_cast<uint32_t*>(p.out + size_t(m) * p.N + n) = pack_bf16x2(x * (a * s0), y * (a * s1));
+    }
+  }
+  if (splits > 1) cluster_sync(); else __syncthreads();  // no CTA leaves while its partial may be read
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, L::kCols);
+  }
+}
+
+}  // namespace fp4
+}  // namespace zi

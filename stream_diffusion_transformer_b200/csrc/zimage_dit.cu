@@ -11,7 +11,9 @@
 #include <vector>
 
 #include "zi_attention.cuh"
+#include "zi_attention_masked.cuh"
 #include "zi_common.cuh"
+#include "zi_fp4.cuh"
 #include "zi_gemm.cuh"
 #include "zi_rows.cuh"
 #include "zimage_dit.h"
@@ -610,6 +612,134 @@ __global__ void exp2_poly_kernel(const float* __restrict__ x, float* __restrict_
   if (two) y[i + 1] = e1;
 }
 
+// ---------------------------------------------------------------- clusters
+
+// Raise a kernel's dynamic shared-memory limit once per device (kernels outside KernelBit).
+template <auto Kern>
+int raise_smem(const DevInfo* d, int bytes) {
+  static bool done[kMaxDevices] = {};
+  std::lock_guard<std::mutex> lk(g_dev_mu);
+  bool& here = done[d - g_dev];
+  if (here) return ZI_OK;
+  if (cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    return ZI_ERR_CUDA;
+  here = true;
+  return ZI_OK;
+}
+
+// Launch with clusters of `cluster` consecutive blocks along x.
+template <auto Kern, typename... Args>
+int launch_clustered(int kind, dim3 grid, int threads, uint32_t smem, int cluster, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = unsigned(cluster);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  prof_pre(st);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, Kern, args...);
+  const int s = launched(kind, st);
+  return e != cudaSuccess ? ZI_ERR_CUDA : s;
+}
+
+// ---------------------------------------------------------------- 4-bit rows
+
+constexpr int kFp4MaxCols = 16384;
+constexpr int kMaxDim = 1 << 24;
+
+template <int FMT, typename TIn>
+int run_quantize_fp4(const TIn* x, int rows, int cols, uint8_t* q, uint8_t* bs, float* rs, cudaStream_t st) {
+  const int spans = cols / 16;
+  int tpr = 8;  // threads per row: a power of two, at least one scale word's
+  while (tpr < spans && tpr < fp4::kRowsThreads) tpr *= 2;
+  const int per = fp4::kRowsThreads / tpr;
+  const int rows_pad = fp4::tiles_down(rows) * 128;
+  const int grid = (rows_pad + per - 1) / per;
+  prof_pre(st);
+  if (spans <= tpr)
+    fp4::quantize_kernel<FMT, TIn, 1><<<grid, fp4::kRowsThreads, 0, st>>>(x, rows, cols, tpr, q, bs, rs);
+  else if (spans <= 2 * tpr)
+    fp4::quantize_kernel<FMT, TIn, 2><<<grid, fp4::kRowsThreads, 0, st>>>(x, rows, cols, tpr, q, bs, rs);
+  else
+    fp4::quantize_kernel<FMT, TIn, 4><<<grid, fp4::kRowsThreads, 0, st>>>(x, rows, cols, tpr, q, bs, rs);
+  return launched(ZI_KERNEL_QUANTIZE_FP4, st);
+}
+
+template <int FMT, typename TOut>
+int run_dequantize_fp4(const uint8_t* q, const uint8_t* bs, const float* rs, int rows, int cols, TOut* y,
+                       cudaStream_t st) {
+  const size_t blocks = (size_t(rows) * (cols / 16) + fp4::kRowsThreads - 1) / fp4::kRowsThreads;
+  if (blocks > size_t(0x7fffffff)) return ZI_ERR_SHAPE;
+  prof_pre(st);
+  fp4::dequantize_kernel<FMT, TOut><<<unsigned(blocks), fp4::kRowsThreads, 0, st>>>(q, bs, rs, rows, cols, y);
+  return launched(ZI_KERNEL_DEQUANTIZE_FP4, st);
+}
+
+// ---------------------------------------------------------------- 4-bit product
+
+template <int FMT, int TN>
+int run_fp4_narrow(DevInfo* dev, const uint8_t* a, const uint8_t* b, const fp4::GemmParams& p, cudaStream_t st) {
+  using L = fp4::NarrowSmem<FMT, TN>;
+  CUtensorMap ta, tb;
+  ZI_TRY(make_map(&ta, a, uint64_t(p.K / 2), uint64_t(p.M), uint64_t(p.K / 2), 128, TN, CU_TENSOR_MAP_DATA_TYPE_UINT8));
+  ZI_TRY(make_map(&tb, b, uint64_t(p.K / 2), uint64_t(p.N), uint64_t(p.K / 2), 128, 128, CU_TENSOR_MAP_DATA_TYPE_UINT8));
+  constexpr auto kern = fp4::gemm_narrow_kernel<FMT, TN>;
+  ZI_TRY((raise_smem<kern>(dev, int(L::kBytes))));
+  const int nt = (p.N + 127) / 128, mt = (p.M + TN - 1) / TN;
+  if (mt > 65535) return ZI_ERR_SHAPE;
+  const int stages = (p.K + fp4::kStageK - 1) / fp4::kStageK;
+  int splits = 1;
+  while (splits < 8 && 2 * splits <= stages && static_cast<long long>(nt) * mt * 2 * splits <= dev->sms) splits *= 2;
+  return launch_clustered<kern>(ZI_KERNEL_GEMM_FP4, dim3(unsigned(nt * splits), unsigned(mt)), fp4::kNarrowThreads,
+                                L::kBytes, splits, st, ta, tb, p, splits);
+}
+
+template <int FMT>
+int run_fp4_gemm(DevInfo* dev, const uint8_t* a, const uint8_t* b, const fp4::GemmParams& p, cudaStream_t st) {
+  if (p.M <= 16) return run_fp4_narrow<FMT, 16>(dev, a, b, p, st);
+  if (p.M <= 32) return run_fp4_narrow<FMT, 32>(dev, a, b, p, st);
+  if (p.M <= 64) return run_fp4_narrow<FMT, 64>(dev, a, b, p, st);
+  return run_fp4_narrow<FMT, 128>(dev, a, b, p, st);
+}
+
+// ---------------------------------------------------------------- masked attention
+
+int run_attention_few(DevInfo* dev, const MaskedParams& p, cudaStream_t st) {
+  constexpr auto kern = attention_few_kernel;
+  ZI_TRY((raise_smem<kern>(dev, int(few::kSmemBytes))));
+  const long long tiles = (static_cast<long long>(p.q_len) * p.group + 15) / 16;
+  const long long units = tiles * p.kv_heads * p.batch;
+  const int chunks = (p.kv_len + few::kChunk - 1) / few::kChunk;
+  int splits = 1;
+  while (splits < 8 && units * 2 * splits <= dev->sms && 2 * splits * few::kWarps <= chunks) splits *= 2;
+  if (tiles * splits > 0x7fffffffLL || p.kv_heads > 65535 || p.batch > 65535) return ZI_ERR_SHAPE;
+  return launch_clustered<kern>(ZI_KERNEL_ATTENTION_MASKED,
+                                dim3(unsigned(tiles * splits), unsigned(p.kv_heads), unsigned(p.batch)), few::kThreads,
+                                few::kSmemBytes, splits, st, p, splits);
+}
+
+// Checks one operand's strides; those of dimensions of size 1 are not read and become 0.
+int check_strides(const void* ptr, int64_t bs, int64_t rs, int64_t hs, int batch, int rows, int heads, long long* out) {
+  if (!ptr) return ZI_ERR_ARG;
+  if (!aligned16(ptr)) return ZI_ERR_ALIGN;
+  const int64_t s[3] = {batch > 1 ? bs : 0, rows > 1 ? rs : 0, heads > 1 ? hs : 0};
+  const int n[3] = {batch, rows, heads};
+  for (int i = 0; i < 3; ++i) {
+    if (n[i] > 1 && s[i] < 128) return ZI_ERR_ARG;
+    if (s[i] % 8) return ZI_ERR_ALIGN;
+    if (s[i] >= (int64_t(1) << 36)) return ZI_ERR_SHAPE;
+    out[i] = s[i];
+  }
+  return ZI_OK;
+}
+
 // ---------------------------------------------------------------- fixed scratch
 // Scratch of zi_block_forward_noalloc: a file-scope device array, so the entry
 // point needs no caller workspace and allocates nothing.  Host code must not use
@@ -837,6 +967,136 @@ int zi_attention_varlen(const uint16_t* d_qkv, uint16_t* d_out, int batch, int s
   const int row0[1] = {0}, len[1] = {seq};
   return run_attention(dev, d_qkv, batch * seq, d_out, heads * 128, heads, batch, 1, row0, len, d_kv_len,
                        reinterpret_cast<cudaStream_t>(stream));
+}
+
+int zi_attention_desc_init(zi_attention_desc* desc) {
+  if (!desc) return ZI_ERR_ARG;
+  memset(desc, 0, sizeof(*desc));
+  desc->scale = float(1.0 / std::sqrt(128.0));
+  return ZI_OK;
+}
+
+int zi_attention_masked(const zi_attention_desc* d, zi_stream_t stream) {
+  if (!d || d->batch <= 0 || d->heads <= 0 || d->kv_heads <= 0 || d->q_len <= 0 || d->kv_len <= 0) return ZI_ERR_ARG;
+  if (!(d->scale > 0.f) || !std::isfinite(d->scale) || !(d->softcap >= 0.f) || !std::isfinite(d->softcap))
+    return ZI_ERR_ARG;
+  if ((d->causal != 0 && d->causal != 1) || (d->d_prefix_len && !d->causal)) return ZI_ERR_ARG;
+  if ((d->d_q_doc == nullptr) != (d->d_k_doc == nullptr)) return ZI_ERR_ARG;
+  if (d->heads % d->kv_heads) return ZI_ERR_SHAPE;
+  if (d->batch > 65535 || d->heads > 65535 || d->q_len > kMaxDim || d->kv_len > kMaxDim) return ZI_ERR_SHAPE;
+  const int group = d->heads / d->kv_heads;
+  if (static_cast<long long>(d->q_len) * group > (1LL << 30)) return ZI_ERR_SHAPE;
+  const void* words[] = {d->d_slopes, d->d_prefix_len, d->d_kv_len, d->d_q_doc, d->d_k_doc};
+  for (const void* w : words)
+    if (reinterpret_cast<uintptr_t>(w) & 3u) return ZI_ERR_ALIGN;
+  MaskedParams p;
+  memset(&p, 0, sizeof(p));
+  long long s[4][3];
+  ZI_TRY(check_strides(d->q, d->q_batch_stride, d->q_row_stride, d->q_head_stride, d->batch, d->q_len, d->heads, s[0]));
+  ZI_TRY(check_strides(d->k, d->k_batch_stride, d->k_row_stride, d->k_head_stride, d->batch, d->kv_len, d->kv_heads,
+                       s[1]));
+  ZI_TRY(check_strides(d->v, d->v_batch_stride, d->v_row_stride, d->v_head_stride, d->batch, d->kv_len, d->kv_heads,
+                       s[2]));
+  ZI_TRY(check_strides(d->out, d->out_batch_stride, d->out_row_stride, d->out_head_stride, d->batch, d->q_len,
+                       d->heads, s[3]));
+  p.q = d->q;
+  p.k = d->k;
+  p.v = d->v;
+  p.out = d->out;
+  p.q_bs = s[0][0], p.q_rs = s[0][1], p.q_hs = s[0][2];
+  p.k_bs = s[1][0], p.k_rs = s[1][1], p.k_hs = s[1][2];
+  p.v_bs = s[2][0], p.v_rs = s[2][1], p.v_hs = s[2][2];
+  p.o_bs = s[3][0], p.o_rs = s[3][1], p.o_hs = s[3][2];
+  p.batch = d->batch;
+  p.heads = d->heads;
+  p.kv_heads = d->kv_heads;
+  p.group = group;
+  p.q_len = d->q_len;
+  p.kv_len = d->kv_len;
+  const double log2e = 1.4426950408889634;
+  p.scale_log2 = d->softcap > 0.f ? float(double(d->scale) / d->softcap) : float(double(d->scale) * log2e);
+  p.cap_log2 = float(double(d->softcap) * log2e);
+  p.slopes = d->d_slopes;
+  p.causal = d->causal;
+  p.prefix = d->d_prefix_len;
+  p.lengths = d->d_kv_len;
+  p.q_doc = d->d_q_doc;
+  p.k_doc = d->d_k_doc;
+  DevInfo* dev;
+  ZI_TRY(current_device(&dev));
+  return run_attention_few(dev, p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int zi_fp4_scale_size(int format, int rows, int cols, size_t* h_bytes) {
+  if ((format != ZI_FP4_MX && format != ZI_FP4_NV) || rows < 0 || cols <= 0 || !h_bytes) return ZI_ERR_ARG;
+  if (cols % 32 || cols > kMaxDim || rows > (1 << 30)) return ZI_ERR_SHAPE;
+  const int x = format == ZI_FP4_MX ? fp4::tiles_along<fp4::MX>(cols) : fp4::tiles_along<fp4::NV>(cols);
+  *h_bytes = size_t(fp4::tiles_down(rows)) * x * fp4::kTileBytes;
+  return ZI_OK;
+}
+
+namespace {
+// The checks that zi_quantize_fp4 and zi_dequantize_fp4 share.
+int check_fp4_rows(int format, const void* x, int flag, int rows, int cols, const void* q, const void* bs,
+                   const void* rs) {
+  if ((format != ZI_FP4_MX && format != ZI_FP4_NV) || !x || !q || !bs || rows < 0 || cols <= 0 ||
+      (flag != 0 && flag != 1))
+    return ZI_ERR_ARG;
+  if ((format == ZI_FP4_NV) != (rs != nullptr)) return ZI_ERR_ARG;
+  if (cols % 32 || cols > kFp4MaxCols || rows > (1 << 30)) return ZI_ERR_SHAPE;
+  if (!aligned16(x) || !aligned16(q) || !aligned16(bs) || !aligned16(rs)) return ZI_ERR_ALIGN;
+  return ZI_OK;
+}
+}  // namespace
+
+int zi_quantize_fp4(int format, const void* d_x, int x_bf16, int rows, int cols, uint8_t* d_q, uint8_t* d_bs,
+                    float* d_rs, zi_stream_t stream) {
+  ZI_TRY(check_fp4_rows(format, d_x, x_bf16, rows, cols, d_q, d_bs, d_rs));
+  DevInfo* dev;
+  ZI_TRY(current_device(&dev));
+  if (rows == 0) return ZI_OK;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const float* xf = static_cast<const float*>(d_x);
+  const uint16_t* xh = static_cast<const uint16_t*>(d_x);
+  if (format == ZI_FP4_MX)
+    return x_bf16 ? run_quantize_fp4<fp4::MX>(xh, rows, cols, d_q, d_bs, d_rs, st)
+                  : run_quantize_fp4<fp4::MX>(xf, rows, cols, d_q, d_bs, d_rs, st);
+  return x_bf16 ? run_quantize_fp4<fp4::NV>(xh, rows, cols, d_q, d_bs, d_rs, st)
+                : run_quantize_fp4<fp4::NV>(xf, rows, cols, d_q, d_bs, d_rs, st);
+}
+
+int zi_dequantize_fp4(int format, const uint8_t* d_q, const uint8_t* d_bs, const float* d_rs, int rows, int cols,
+                      void* d_y, int y_bf16, zi_stream_t stream) {
+  ZI_TRY(check_fp4_rows(format, d_y, y_bf16, rows, cols, d_q, d_bs, d_rs));
+  DevInfo* dev;
+  ZI_TRY(current_device(&dev));
+  if (rows == 0) return ZI_OK;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  float* yf = static_cast<float*>(d_y);
+  uint16_t* yh = static_cast<uint16_t*>(d_y);
+  if (format == ZI_FP4_MX)
+    return y_bf16 ? run_dequantize_fp4<fp4::MX>(d_q, d_bs, d_rs, rows, cols, yh, st)
+                  : run_dequantize_fp4<fp4::MX>(d_q, d_bs, d_rs, rows, cols, yf, st);
+  return y_bf16 ? run_dequantize_fp4<fp4::NV>(d_q, d_bs, d_rs, rows, cols, yh, st)
+                : run_dequantize_fp4<fp4::NV>(d_q, d_bs, d_rs, rows, cols, yf, st);
+}
+
+int zi_gemm_fp4(int format, const uint8_t* d_a, const uint8_t* d_abs, const float* d_ars, const uint8_t* d_b,
+                const uint8_t* d_bbs, const float* d_brs, uint16_t* d_c, int m, int n, int k, zi_stream_t stream) {
+  if ((format != ZI_FP4_MX && format != ZI_FP4_NV) || !d_a || !d_abs || !d_b || !d_bbs || !d_c || m < 0 || n <= 0 ||
+      k <= 0)
+    return ZI_ERR_ARG;
+  if ((format == ZI_FP4_NV) != (d_ars != nullptr) || (format == ZI_FP4_NV) != (d_brs != nullptr)) return ZI_ERR_ARG;
+  if (k % 32 || n % 8 || m > kMaxDim || n > kMaxDim || k > kMaxDim) return ZI_ERR_SHAPE;
+  const void* ps[] = {d_a, d_abs, d_ars, d_b, d_bbs, d_brs, d_c};
+  for (const void* q : ps)
+    if (!aligned16(q)) return ZI_ERR_ALIGN;
+  DevInfo* dev;
+  ZI_TRY(current_device(&dev));
+  if (m == 0) return ZI_OK;
+  const fp4::GemmParams p{d_abs, d_bbs, d_ars, d_brs, d_c, m, n, k};
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return format == ZI_FP4_MX ? run_fp4_gemm<fp4::MX>(dev, d_a, d_b, p, st) : run_fp4_gemm<fp4::NV>(dev, d_a, d_b, p, st);
 }
 
 int zi_block_forward(const zi_config* cfg, const zi_block_weights* w, const float* d_c, const int32_t* d_pos,

@@ -6,7 +6,7 @@ forward runs in libzimage_dit.so.  bf16 tensors are handed over as raw bits.
 from __future__ import annotations
 
 import ctypes
-from typing import Callable, Dict, Iterable, List, Optional, Sequence
+from typing import Callable, Dict, Iterable, List, NamedTuple, Optional, Sequence
 
 import numpy as np
 import torch
@@ -406,6 +406,135 @@ def gemm_e4m3(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch.Tens
     if out is None:
         out = torch.empty((M, N), dtype=torch.bfloat16, device=a.device)
     abi.call("zi_gemm_e4m3", _p(a), _p(sa), _p(b), _p(sb), _p(out), M, N, K, _stream())
+    return out
+
+
+class Fp4Matrix(NamedTuple):
+    """A [rows, cols] matrix in 4 bits: codes uint8 [rows, cols / 2], block scales in the tensor
+    core's tiled layout (uint8, zi_fp4_scale_size bytes) and, for "nvfp4", fp32 row scales [rows]."""
+    fmt: str  # "mxfp4" or "nvfp4"
+    codes: torch.Tensor
+    block_scales: torch.Tensor
+    row_scales: Optional[torch.Tensor] = None
+
+    @property
+    def shape(self):
+        return self.codes.shape[0], 2 * self.codes.shape[1]
+
+
+_FP4_FORMATS = {"mxfp4": abi.ZI_FP4_MX, "nvfp4": abi.ZI_FP4_NV}
+
+
+def _fp4_format(fmt: str) -> int:
+    if fmt not in _FP4_FORMATS:
+        raise ValueError(f"unknown 4-bit format {fmt!r}: one of {sorted(_FP4_FORMATS)}")
+    return _FP4_FORMATS[fmt]
+
+
+def _fp4_check(m: Fp4Matrix) -> int:
+    """The library's number of m's format, after checking m's tensors (the library sees pointers only)."""
+    f = _fp4_format(m.fmt)
+    rows, cols = m.shape
+    parts = [("codes", m.codes, torch.uint8, None), ("block_scales", m.block_scales, torch.uint8,
+                                                     abi.fp4_scale_size(f, rows, cols))]
+    if (m.row_scales is not None) != (f == abi.ZI_FP4_NV):
+        raise ValueError("row_scales belong to nvfp4 and to nvfp4 alone")
+    if f == abi.ZI_FP4_NV:
+        parts.append(("row_scales", m.row_scales, torch.float32, rows))
+    for name, t, dtype, n in parts:
+        if t.dtype != dtype or not t.is_contiguous() or t.device != m.codes.device or not t.is_cuda:
+            raise ValueError(f"{name}: a contiguous {dtype} tensor on the matrix's GPU is needed")
+        if n is not None and t.numel() != n:
+            raise ValueError(f"{name}: {t.numel()} elements, {n} are needed for {rows} x {cols} in {m.fmt}")
+    return f
+
+
+def quantize_fp4(x: torch.Tensor, fmt: str = "nvfp4") -> Fp4Matrix:
+    """The rows of a 2-D fp32 or bf16 tensor in 4 bits (zi_quantize_fp4)."""
+    f = _fp4_format(fmt)
+    if x.dim() != 2 or not x.is_cuda or not x.is_contiguous() or x.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("quantize_fp4: a contiguous 2-D fp32 or bf16 tensor on a GPU is needed")
+    rows, cols = x.shape
+    with torch.cuda.device(x.device):
+        q = torch.empty((rows, cols // 2), dtype=torch.uint8, device=x.device)
+        bs = torch.empty(abi.fp4_scale_size(f, rows, cols), dtype=torch.uint8, device=x.device)
+        rs = torch.empty(rows, dtype=torch.float32, device=x.device) if f == abi.ZI_FP4_NV else None
+        if rows:
+            abi.call("zi_quantize_fp4", f, _p(x), 1 if x.dtype == torch.bfloat16 else 0, rows, cols, _p(q), _p(bs),
+                     _p(rs), _stream())
+    return Fp4Matrix(fmt, q, bs, rs)
+
+
+def dequantize_fp4(m: Fp4Matrix, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """The values that a 4-bit matrix stands for, bf16 or fp32 [rows, cols] (zi_dequantize_fp4)."""
+    f = _fp4_check(m)
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("dequantize_fp4: fp32 or bf16")
+    rows, cols = m.shape
+    with torch.cuda.device(m.codes.device):
+        y = torch.empty((rows, cols), dtype=dtype, device=m.codes.device)
+        if rows:
+            abi.call("zi_dequantize_fp4", f, _p(m.codes), _p(m.block_scales), _p(m.row_scales), rows, cols, _p(y),
+                     1 if dtype == torch.bfloat16 else 0, _stream())
+    return y
+
+
+def gemm_fp4(a: Fp4Matrix, b: Fp4Matrix, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """bf16 [M, N] = a [M, K] b [N, K]^T of two 4-bit matrices of one format (zi_gemm_fp4)."""
+    f = _fp4_check(a)
+    if _fp4_check(b) != f or a.shape[1] != b.shape[1] or a.codes.device != b.codes.device:
+        raise ValueError("gemm_fp4: two matrices of one format, one K and one device are needed")
+    (M, K), N = a.shape, b.shape[0]
+    with torch.cuda.device(a.codes.device):
+        if out is None:
+            out = torch.empty((M, N), dtype=torch.bfloat16, device=a.codes.device)
+        elif (tuple(out.shape) != (M, N) or out.dtype != torch.bfloat16 or not out.is_contiguous()
+              or out.device != a.codes.device):
+            raise ValueError("gemm_fp4: out has to be a contiguous bf16 [M, N] tensor on the operands' GPU")
+        if M:
+            abi.call("zi_gemm_fp4", f, _p(a.codes), _p(a.block_scales), _p(a.row_scales), _p(b.codes),
+                     _p(b.block_scales), _p(b.row_scales), _p(out), M, N, K, _stream())
+    return out
+
+
+def attention_masked(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, scale: Optional[float] = None,
+                     softcap: float = 0.0, slopes: Optional[torch.Tensor] = None, causal: bool = False,
+                     prefix_len: Optional[torch.Tensor] = None, kv_len: Optional[torch.Tensor] = None,
+                     q_doc: Optional[torch.Tensor] = None, k_doc: Optional[torch.Tensor] = None,
+                     out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Attention with capped scores, a distance bias and masks (zi_attention_masked).
+
+    q bf16 [B, q_len, H, 128], k and v bf16 [B, kv_len, Hk, 128] with H a multiple of Hk, in any
+    strides with contiguous heads; returns bf16 [B, q_len, H, 128].  softcap 0 = none; slopes fp32 [H];
+    prefix_len (with causal) and kv_len int32 [B]; q_doc int32 [B, q_len] with k_doc int32 [B, kv_len]."""
+    if q.dim() != 4 or k.dim() != 4 or k.shape != v.shape or q.shape[0] != k.shape[0] or q.shape[3] != 128 \
+            or k.shape[3] != 128:
+        raise ValueError("attention_masked: q [B, q_len, H, 128] and k, v [B, kv_len, Hk, 128] are needed")
+    B, n, H, _ = q.shape
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    elif out.shape != q.shape:
+        raise ValueError("attention_masked: out has to have q's shape")
+    d = abi.attention_desc_init()
+    for name, t in (("q", q), ("k", k), ("v", v), ("out", out)):
+        if t.dtype != torch.bfloat16 or not t.is_cuda or t.device != q.device or t.stride(3) != 1:
+            raise ValueError(f"attention_masked: {name} has to be bf16 with contiguous heads on q's GPU")
+        setattr(d, name, t.data_ptr())
+        for i, dim in enumerate(("batch", "row", "head")):
+            setattr(d, f"{name}_{dim}_stride", t.stride(i))
+    d.batch, d.heads, d.kv_heads, d.q_len, d.kv_len = B, H, k.shape[2], n, k.shape[1]
+    if scale is not None:
+        d.scale = float(scale)
+    d.softcap, d.causal = float(softcap), 1 if causal else 0
+    for name, t, dtype, shape in (("slopes", slopes, torch.float32, (H,)), ("prefix_len", prefix_len, torch.int32, (B,)),
+                                  ("kv_len", kv_len, torch.int32, (B,)), ("q_doc", q_doc, torch.int32, (B, n)),
+                                  ("k_doc", k_doc, torch.int32, (B, k.shape[1]))):
+        if t is not None:
+            if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != q.device:
+                raise ValueError(f"attention_masked: {name} has to be a contiguous {dtype} tensor {shape} on q's GPU")
+            setattr(d, f"d_{name}", t.data_ptr())
+    with torch.cuda.device(q.device):
+        abi.call("zi_attention_masked", ctypes.byref(d), _stream())
     return out
 
 
