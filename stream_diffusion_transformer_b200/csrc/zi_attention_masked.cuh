@@ -6,6 +6,7 @@
 // and i sees j when j < n_b, and (causal) j <= p_i or j < prefix_b, and (documents) their
 // ids are equal and not negative.
 #pragma once
+#include "zi_attention.cuh"
 #include "zi_common.cuh"
 
 namespace zi {
@@ -323,6 +324,661 @@ __global__ void __launch_bounds__(few::kThreads) attention_few_kernel(MaskedPara
     p.out[b * p.o_bs + i * p.o_rs + (hk * p.group + g) * p.o_hs + d] = *reinterpret_cast<const uint16_t*>(&yb);
   }
   if (splits > 1) cluster_sync();  // no CTA leaves while its partial may be read
+}
+
+// ------------------------------------------------------------------ many queries
+// Flash attention on tcgen05, laid out as attention_kernel is (two 128-row tiles A and B per
+// CTA, S and O of both in TMEM, P written back over its S, one softmax thread per row), with
+// - a row = one query of one head of a key head's group, packed as for few queries: the
+//   heads that share keys share the CTA's K and V tiles, and a causal tile spans fewer queries;
+// - Q written to smem by the row threads (any strides), K and V tiles by TMA;
+// - key tiles that no row of the CTA sees left out (by the rows' limits, and by the ranges of
+//   document ids of the tile and of the rows), elementwise masks only on tiles that some row
+//   sees in part;
+// - V rows that no query may see (past the element's keys, or with a negative id) cleared in
+//   smem before the product: zero probabilities times NaN would be NaN;
+// - with few CTAs, a cluster that shares a unit's keys and joins its partials through
+//   distributed shared memory in rank order (no workspace, no atomics).
+// Warps 0..3 rows of tile A, 4..7 of tile B, 8 K loads, 9 MMA, 10 V loads, 11 clears V.
+namespace many {
+constexpr int kThreads = 384;
+constexpr int kRegsSoftmax = 216, kRegsOther = 56;  // as attention_kernel: 62464 <= 384 x 168 registers at launch
+constexpr uint32_t kTile = 128 * 128 * 2, kHalf = kTile / 2;
+constexpr int kKSlots = 3, kVSlots = 2;
+constexpr uint32_t kQ0 = 0, kK0 = 2 * kTile, kV0 = kK0 + kKSlots * kTile;
+constexpr uint32_t kBar = kV0 + kVSlots * kTile;
+constexpr int kListTiles = 4096;  // key tiles whose state fits the list (2 bits each); later ones are masked elementwise
+constexpr uint32_t kList = kBar + 256;
+constexpr uint32_t kSmemBytes = kList + kListTiles / 4 + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory");
+constexpr uint32_t kColS = 0, kColO = 256;
+// the partial of a split unit, over K and V: O [t][32 column quads][128 rows] float4, then (m, l) [256] float2
+constexpr uint32_t kPart = kK0;
+static_assert(kPart + 2 * 32 * 128 * 16 + 256 * 8 <= kBar, "partials fit the rings");
+}  // namespace many
+
+// tanh on [-1, 1] as z P(z^2) for a pair on the FMA pipe: a degree-9 odd polynomial fitted
+// here by the Remez exchange on the absolute error (2.8e-6 at most).  c: P's coefficients times
+// the cap, so the result is cap tanh(z).
+ZI_DEV uint64_t cap_poly_pair(uint64_t z2, const float* c) {
+  const uint64_t u = f2_mul(z2, z2);
+  uint64_t r = f2_fma(f2_pack(c[4], c[4]), u, f2_pack(c[3], c[3]));
+  r = f2_fma(r, u, f2_pack(c[2], c[2]));
+  r = f2_fma(r, u, f2_pack(c[1], c[1]));
+  r = f2_fma(r, u, f2_pack(c[0], c[0]));
+  return f2_mul(r, z2);
+}
+
+ZI_DEV void tma_load_4d(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::
+          "r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+
+ZI_DEV float ld_cluster_f32(uint32_t addr, int rank) {
+  float x;
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(a) : "memory");
+  return x;
+}
+ZI_DEV float4 ld_cluster_f4(uint32_t addr, int rank) {
+  float4 x;
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+               : "r"(a)
+               : "memory");
+  return x;
+}
+
+// The low word of a 128-byte-swizzled operand descriptor (smem_desc_sw128); its high word is
+// the same for every tile.  Kept opaque to the compiler: it would otherwise hold the sixteen
+// descriptors of both Q tiles across the loop, spill them from the MMA warp's 56 registers and
+// slow the issue of every MMA (measured: 2.5 us a key step against 2.2).
+ZI_DEV uint32_t desc_low(uint32_t saddr, uint32_t lead_bytes) {
+  uint32_t lo = ((saddr & 0x3FFFFu) >> 4) | ((lead_bytes >> 4) << 16);
+  asm volatile("" : "+r"(lo));
+  return lo;
+}
+ZI_DEV uint64_t desc_at(uint32_t low, uint32_t bytes) {
+  constexpr uint32_t kHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(low + (bytes >> 4)), "r"(kHigh));
+  return d;
+}
+
+template <bool CAP, bool BIAS>
+__global__ void __launch_bounds__(many::kThreads, 1)
+    attention_many_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                          MaskedParams p, int splits) {
+  using namespace many;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kBar);
+  uint64_t* k_full = bars + 0;    // [kKSlots]
+  uint64_t* k_empty = bars + 3;   // [kKSlots]
+  uint64_t* v_full = bars + 6;    // [kVSlots]
+  uint64_t* v_empty = bars + 8;   // [kVSlots]
+  uint64_t* v_clean = bars + 10;  // [kVSlots]
+  uint64_t* s_full = bars + 12;   // [2 tiles]
+  uint64_t* p_full = bars + 14;   // [2 tiles]
+  uint64_t* pv_done = bars + 16;  // [2 tiles]
+  uint64_t* drain = bars + 18;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 19);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* lim_min = reinterpret_cast<int*>(tmem_slot + 2);
+  int* lim_max = lim_min + 1;
+  int* doc_min = lim_min + 2;  // of the rows' ids that are not negative ...
+  int* doc_max = lim_min + 3;
+  int* doc_neg = lim_min + 4;  // ... and whether any is
+  uint32_t* list = reinterpret_cast<uint32_t*>(smem + kList);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = int(blockIdx.x) % splits;
+  const int units_x = int(gridDim.x) / splits;
+  const int unit = units_x - 1 - int(blockIdx.x) / splits;  // with a causal mask the last rows have the most keys: first
+  const int hk = blockIdx.y, b = blockIdx.z;
+  const int rows = p.q_len * p.group;
+  const int row0 = unit * 256;
+  const bool has_b = row0 + 128 < rows;
+  const int n = masked_keys(p, b);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kKSlots; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
+      mbar_init(&v_clean[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);  // one arrival per softmax warp
+      mbar_init(&pv_done[i], 1);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = device_error_set() ? 1 : 0;  // an earlier kernel timed out: leave everything untouched
+    *lim_min = 0x7fffffff;
+    *lim_max = 0;
+    *doc_min = 0x7fffffff;
+    *doc_max = -1;
+    *doc_neg = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8 && lane == 0) {
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
+  }
+  if (warp == 9) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const bool skip = *abort_flag != 0;
+
+  // the row threads: what their row sees, and its Q to smem
+  const int row = row0 + int(threadIdx.x);
+  const int qi = row / p.group, qg = row - qi * p.group;
+  int lim = 0, doc = 0;
+  if (warp < 8) {
+    const bool have = row < rows;
+    int d_lo = 0x7fffffff, d_hi = -1, neg = 0;
+    if (have) {
+      lim = masked_limit(p, b, qi, n);
+      if (p.q_doc) {
+        doc = __ldg(p.q_doc + size_t(b) * p.q_len + qi);
+        if (doc < 0) {
+          lim = 0;
+          neg = 1;
+        } else {
+          d_lo = d_hi = doc;
+        }
+      }
+    }
+    const int lo = __reduce_min_sync(0xffffffffu, have ? lim : 0x7fffffff);
+    const int hi = __reduce_max_sync(0xffffffffu, lim);
+    d_lo = __reduce_min_sync(0xffffffffu, d_lo);
+    d_hi = __reduce_max_sync(0xffffffffu, d_hi);
+    neg = __reduce_max_sync(0xffffffffu, neg);
+    if (lane == 0) {
+      atomicMin(lim_min, lo);
+      atomicMax(lim_max, hi);
+      atomicMin(doc_min, d_lo);
+      atomicMax(doc_max, d_hi);
+      atomicMax(doc_neg, neg);
+    }
+    // this warp's 32 rows of Q, half a warp per row (256 contiguous bytes)
+    const long long at = have ? b * p.q_bs + qi * p.q_rs + (hk * p.group + qg) * p.q_hs : -1;
+    const int x = lane & 15;
+#pragma unroll
+    for (int r0 = 0; r0 < 32; r0 += 16) {
+      uint4 w[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const long long src = __shfl_sync(0xffffffffu, at, r0 + 2 * e + (lane >> 4));
+        w[e] = src >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.q + src) + x) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int i = (warp & 3) * 32 + r0 + 2 * e + (lane >> 4);
+        *reinterpret_cast<uint4*>(smem + kQ0 + (warp >> 2) * kTile + (x >> 3) * kHalf + i * 128 +
+                                  (((x & 7) ^ (i & 7)) << 4)) = w[e];
+      }
+    }
+    fence_proxy_async_smem();
+  }
+  __syncthreads();
+  const int tiles = (*lim_max + 127) / 128;  // key tiles that any row of the CTA may see
+  const int all_lim = *lim_min;
+  const int* kd = p.k_doc ? p.k_doc + size_t(b) * p.kv_len : nullptr;
+  const int my_j0 = int(static_cast<long long>(rank) * tiles / splits);
+  const int my_j1 = int(static_cast<long long>(rank + 1) * tiles / splits);
+  // tile states, 2 bits each, 16 tiles a word: 0 no row sees any key, 1 every row sees every key, 2 between
+  if (kd) {
+    const int q_lo = *doc_min, q_hi = *doc_max;
+    const bool q_one = q_lo == q_hi && *doc_neg == 0;
+    for (int w = (my_j0 >> 4) + int(threadIdx.x); w * 16 < my_j1 && w < kListTiles / 16; w += kThreads) list[w] = 0;
+    __syncthreads();
+    constexpr int kWarps = kThreads / 32, kAhead = 3;  // tiles of ids in flight per warp
+    for (int j = my_j0 + warp; j < my_j1 && j < kListTiles; j += kWarps * kAhead) {
+      int d[kAhead][4];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int key = (j + u * kWarps) * 128 + e * 32 + lane;
+          d[u][e] = key < n ? __ldg(kd + key) : -1;
+        }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int jj = j + u * kWarps;
+        int lo = 0x7fffffff, hi = -1, neg = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (d[u][e] < 0) neg = 1;
+          else lo = min(lo, d[u][e]);
+          hi = max(hi, d[u][e]);
+        }
+        lo = __reduce_min_sync(0xffffffffu, lo);
+        hi = __reduce_max_sync(0xffffffffu, hi);
+        neg = __reduce_max_sync(0xffffffffu, neg);
+        const bool none = hi < q_lo || lo > q_hi;
+        const bool full = q_one && !neg && lo == hi && lo == q_lo && (jj + 1) * 128 <= all_lim;
+        if (lane == 0 && !none && jj < my_j1 && jj < kListTiles) atomicOr(list + (jj >> 4), (full ? 1u : 2u) << (2 * (jj & 15)));
+      }
+    }
+    __syncthreads();
+  }
+  auto state = [&](int j) -> uint32_t {
+    if (kd) return j < kListTiles ? (list[j >> 4] >> (2 * (j & 15))) & 3u : 2u;
+    return (j + 1) * 128 <= all_lim ? 1u : 2u;
+  };
+  // the next tile of this CTA at or after j that some row sees (my_j1: none)
+  auto next = [&](int j) -> int {
+    if (kd)
+      while (j < my_j1 && state(j) == 0) ++j;
+    return j;
+  };
+  const int first = skip ? my_j1 : next(my_j0);
+  const bool clean = p.lengths != nullptr || kd != nullptr;  // V may hold rows that nobody sees
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if (warp == 8 || warp == 10) {
+      if (lane == 0) {
+        const bool kq = warp == 8;
+        uint64_t* fullb = kq ? k_full : v_full;
+        uint64_t* emptyb = kq ? k_empty : v_empty;
+        const CUtensorMap* map = kq ? &tmK : &tmV;
+        const uint32_t base = kq ? kK0 : kV0;
+        const int nslots = kq ? kKSlots : kVSlots;
+        int it = 0;
+        bool ok = true;
+        for (int j = first; j < my_j1; j = next(j + 1), ++it) {
+          const int bi = it % nslots;
+          if (!mbar_wait(&emptyb[bi], (uint32_t(it / nslots) & 1u) ^ 1u, abort_flag, ZI_DEVERR_TIMEOUT_PRODUCER)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&fullb[bi], kTile);
+          tma_load_4d(smem + base + bi * kTile, map, &fullb[bi], 0, hk, j * 128, b);
+          tma_load_4d(smem + base + bi * kTile + kHalf, map, &fullb[bi], 64, hk, j * 128, b);
+        }
+        if (!ok) {
+          volatile int never = 0;
+          for (int k = it > nslots ? it - nslots : 0; k < it; ++k)
+            mbar_wait(&fullb[k % nslots], uint32_t(k / nslots) & 1u, &never, ZI_DEVERR_TIMEOUT_DRAIN);
+        }
+      }
+    } else if (warp == 9) {
+      int count = skip ? 0 : my_j1 - my_j0;  // tiles of this CTA that some row sees
+      if (kd && count > 0) {
+        count = 0;
+        for (int j = my_j0 + lane; j < my_j1; j += 32) count += state(j) != 0 ? 1 : 0;
+        count = __reduce_add_sync(0xffffffffu, count);
+      }
+      if (lane == 0 && count > 0) {
+        constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
+        constexpr uint32_t idesc_o = idesc_bf16_f32(128, 128, false, true);
+        auto issue_s = [&](int t, int it) {
+          const uint32_t q_low = desc_low(smem_u32(smem + kQ0 + t * kTile), 16);
+          const uint32_t k_low = desc_low(smem_u32(smem + kK0 + (it % kKSlots) * kTile), 16);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t at = (k >> 2) * kHalf + (k & 3) * 32;
+            tc_mma(tmem + kColS + 128 * t, desc_at(q_low, at), desc_at(k_low, at), idesc_s, k > 0 ? 1u : 0u);
+          }
+          tc_commit(&s_full[t]);
+        };
+        auto issue_pv = [&](int t, int it) -> bool {
+          if (!mbar_wait(&p_full[t], uint32_t(it) & 1u, abort_flag, ZI_DEVERR_TIMEOUT_MMA)) return false;
+          tc_fence_after();
+          const uint32_t v_low = desc_low(smem_u32(smem + kV0 + (it & 1) * kTile), kHalf);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            tc_mma_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + 8 * k, desc_at(v_low, k * 2048), idesc_o,
+                      (it > 0 || k > 0) ? 1u : 0u);
+          tc_commit(&pv_done[t]);
+          return true;
+        };
+        auto wait_k = [&](int it) {
+          return mbar_wait(&k_full[it % kKSlots], uint32_t(it / kKSlots) & 1u, abort_flag, ZI_DEVERR_TIMEOUT_MMA);
+        };
+        auto wait_v = [&](int it) {
+          const uint32_t phase = (uint32_t(it) >> 1) & 1u;
+          return mbar_wait(&v_full[it & 1], phase, abort_flag, ZI_DEVERR_TIMEOUT_MMA) &&
+                 (!clean || mbar_wait(&v_clean[it & 1], phase, abort_flag, ZI_DEVERR_TIMEOUT_MMA));
+        };
+        bool ok = wait_k(0);
+        if (ok) {
+          tc_fence_after();
+          issue_s(0, 0);
+          if (has_b) issue_s(1, 0);
+          tc_commit(&k_empty[0]);
+          ok = wait_v(0) && issue_pv(0, 0);
+        }
+        for (int it = 0; it < count && ok; ++it) {
+          const bool more = it + 1 < count;
+          if (more) {
+            if (!wait_k(it + 1)) { ok = false; break; }
+            tc_fence_after();
+            issue_s(0, it + 1);
+          }
+          if (has_b && !issue_pv(1, it)) { ok = false; break; }
+          tc_commit(&v_empty[it & 1]);
+          if (more) {
+            if (has_b) issue_s(1, it + 1);
+            tc_commit(&k_empty[(it + 1) % kKSlots]);
+            if (!wait_v(it + 1) || !issue_pv(0, it + 1)) { ok = false; break; }
+          }
+        }
+        if (!ok) {
+          tc_commit(drain);
+          volatile int never = 0;
+          mbar_wait(drain, 0, &never, ZI_DEVERR_TIMEOUT_DRAIN);
+        }
+      }
+    } else if (clean) {
+      int it = 0;
+      for (int j = first; j < my_j1; j = next(j + 1), ++it) {
+        if (!mbar_wait(&v_full[it & 1], (uint32_t(it) >> 1) & 1u, abort_flag, ZI_DEVERR_TIMEOUT_SOFTMAX)) break;
+        if (state(j) != 1) {
+          uint8_t* v = smem + kV0 + (it & 1) * kTile;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int r = e * 32 + lane, key = j * 128 + r;
+            if (key >= n || (kd && __ldg(kd + key) < 0)) {
+#pragma unroll
+              for (int x = 0; x < 8; ++x) {
+                *reinterpret_cast<uint4*>(v + r * 128 + x * 16) = make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4*>(v + kHalf + r * 128 + x * 16) = make_uint4(0, 0, 0, 0);
+              }
+            }
+          }
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&v_clean[it & 1]);
+      }
+    }
+    __syncwarp();
+    if (splits > 1) {
+      cluster_sync();
+      cluster_sync();
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    const int t = warp >> 2, q = warp & 3;
+    const int i = q * 32 + lane;
+    const uint32_t lane_addr = tmem + (uint32_t(q * 32) << 16);
+    const uint32_t s_addr = lane_addr + kColS + 128 * t;
+    const uint32_t o_addr = lane_addr + kColO + 128 * t;
+    float m_run = -INFINITY, l = 0.f;
+    bool ok = !skip;
+    int it = 0;
+    if (t == 0 || has_b) {
+      const float slope = BIAS && row < rows ? __ldg(p.slopes + hk * p.group + qg) * 1.4426950408889634f : 0.f;
+      const float pos = float(qi + n - p.q_len);
+      float cc[5];
+      if constexpr (CAP) {
+        cc[0] = 0.9999684695f * p.cap_log2;
+        cc[1] = -0.332658232f * p.cap_log2;
+        cc[2] = 0.1292206686f * p.cap_log2;
+        cc[3] = -0.0432998637f * p.cap_log2;
+        cc[4] = 0.008365886568f * p.cap_log2;
+      }
+      uint32_t s[128];
+      for (int j = first; ok && j < my_j1; j = next(j + 1), ++it) {
+        if (!mbar_wait(&s_full[t], uint32_t(it) & 1u, abort_flag, ZI_DEVERR_TIMEOUT_SOFTMAX)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + c * 32, &s[c * 32]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) reg_fence32(&s[c * 32]);
+        if constexpr (CAP) {
+          // |z| <= 1 over the warp's rows: the polynomial; else (scores past the cap) through exp and a
+          // reciprocal.  NaN (a key row that nobody sees) fails neither comparison's result: it is masked below.
+          float mx = 0.f;
+#pragma unroll
+          for (int c = 0; c < 128; c += 2)
+            mx = max3f(mx, fabsf(__uint_as_float(s[c])), fabsf(__uint_as_float(s[c + 1])));
+          const uint64_t k2 = f2_pack(p.scale_log2, p.scale_log2);
+          if (__all_sync(0xffffffffu, mx * p.scale_log2 <= 1.f)) {
+#pragma unroll
+            for (int c = 0; c < 64; ++c) {
+              const uint64_t z = f2_mul(f2_pack(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), k2);
+              float y0, y1;
+              f2_unpack(cap_poly_pair(z, cc), y0, y1);
+              s[2 * c] = __float_as_uint(y0);
+              s[2 * c + 1] = __float_as_uint(y1);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+              s[c] = __float_as_uint(tanh_exp(__uint_as_float(s[c]) * p.scale_log2) * p.cap_log2);
+          }
+        }
+        if constexpr (BIAS) {
+          const float away = pos - float(j * 128);
+#pragma unroll
+          for (int c = 0; c < 128; ++c) {
+            const float y = CAP ? __uint_as_float(s[c]) : __uint_as_float(s[c]) * p.scale_log2;
+            s[c] = __float_as_uint(fmaf(-slope, fabsf(away - float(c)), y));
+          }
+        }
+        if (state(j) != 1) {
+          // bit c of vis: the row sees key j 128 + c
+          uint32_t vis[4];
+          const int left = lim - j * 128;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) vis[w] = left >= 32 * w + 32 ? ~0u : left <= 32 * w ? 0u : (1u << (left - 32 * w)) - 1u;
+          if (kd) {
+            int id[4];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const int key = j * 128 + w * 32 + lane;
+              id[w] = key < n ? __ldg(kd + key) : -1;
+            }
+            const int doc0 = __shfl_sync(0xffffffffu, doc, 0);
+            if (__all_sync(0xffffffffu, doc == doc0)) {
+#pragma unroll
+              for (int w = 0; w < 4; ++w) vis[w] &= __ballot_sync(0xffffffffu, id[w] == doc0);
+            } else {
+#pragma unroll 1
+              for (int r = 0; r < 32; ++r) {
+                const int dr = __shfl_sync(0xffffffffu, doc, r);
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                  const uint32_t m = __ballot_sync(0xffffffffu, id[w] == dr);
+                  if (r == lane) vis[w] &= m;
+                }
+              }
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (!(vis[c >> 5] >> (c & 31) & 1u)) s[c] = __float_as_uint(-INFINITY);
+        }
+        const float sl2 = CAP || BIAS ? 1.f : p.scale_log2;  // scores are in the exp2 domain already, or scaled on the way
+        float mx8[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mx8[k] = __uint_as_float(s[k]);
+#pragma unroll
+        for (int c = 8; c < 120; c += 16) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) mx8[k] = max3f(mx8[k], __uint_as_float(s[c + k]), __uint_as_float(s[c + 8 + k]));
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mx8[k] = fmaxf(mx8[k], __uint_as_float(s[120 + k]));
+        const float mx = max3f(max3f(mx8[0], mx8[1], mx8[2]), max3f(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
+        const float m_new = fmaxf(m_run, mx * sl2);
+        // each row moves its maximum by its own scores alone, so its result does not depend on its neighbours
+        const bool grows = m_new > m_run + 8.0f;
+        const bool resc = __any_sync(0xffffffffu, grows);
+        float alpha = 1.0f;
+        if (grows) {
+          alpha = m_run == -INFINITY ? 0.f : fast_exp2(m_run - m_new);  // a row that has seen nothing yet holds nothing
+          m_run = m_new;
+          l *= alpha;
+        }
+        const float m_use = m_run == -INFINITY ? 0.f : m_run;
+        const uint64_t sl2x2 = f2_pack(sl2, sl2), negm = f2_pack(-m_use, -m_use);
+        uint64_t sum2[4] = {0, 0, 0, 0};
+        uint32_t pw[64];
+#pragma unroll
+        for (int c = 0; c < 64; ++c) {
+          float x0, x1;
+          const uint64_t s2 = f2_pack(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]));
+          f2_unpack(CAP || BIAS ? f2_add(s2, negm) : f2_fma(s2, sl2x2, negm), x0, x1);
+          float e0, e1;
+          if ((c & 7) == 1 || (c & 7) == 4 || (c & 7) == 6) {  // 3 of 8 pairs on the FMA pipe
+            exp2_poly_pair(x0, x1, e0, e1);
+          } else {
+            e0 = fast_exp2(x0);
+            e1 = fast_exp2(x1);
+          }
+          sum2[c & 3] = f2_add(sum2[c & 3], f2_pack(e0, e1));
+          pw[c] = pack_bf16x2(e0, e1);
+        }
+        {
+          float a0, a1, b0, b1, c0, c1, d0, d1;
+          f2_unpack(sum2[0], a0, a1);
+          f2_unpack(sum2[1], b0, b1);
+          f2_unpack(sum2[2], c0, c1);
+          f2_unpack(sum2[3], d0, d1);
+          l += ((a0 + a1) + (b0 + b1)) + ((c0 + c1) + (d0 + d1));
+        }
+        if (resc && it > 0) {
+          if (!mbar_wait(&pv_done[t], uint32_t(it - 1) & 1u, abort_flag, ZI_DEVERR_TIMEOUT_SOFTMAX)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t a2 = f2_pack(alpha, alpha);
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            tmem_ld32_sync(o_addr + c * 32, o);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              float y0, y1;
+              f2_unpack(f2_mul(f2_pack(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1])), a2), y0, y1);
+              o[2 * k] = __float_as_uint(y0);
+              o[2 * k + 1] = __float_as_uint(y1);
+            }
+            tmem_st32(o_addr + c * 32, o);
+          }
+        }
+        tmem_st32(s_addr, &pw[0]);
+        tmem_st32(s_addr + 32, &pw[32]);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[t]);  // for the whole warp: its stores are complete
+      }
+      if (ok && it > 0) {
+        ok = mbar_wait(&pv_done[t], uint32_t(it - 1) & 1u, abort_flag, ZI_DEVERR_TIMEOUT_SOFTMAX);
+        if (ok) tc_fence_after();
+      }
+    }
+    const bool live = row < rows;
+    uint16_t* orow = p.out + b * p.o_bs + qi * p.o_rs + (hk * p.group + qg) * p.o_hs;
+    if (splits == 1) {
+      const float inv = m_run == -INFINITY ? 0.f : 1.0f / l;  // a row that sees no key: zeros
+      if (ok && (t == 0 || has_b)) {
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[32];
+          if (it > 0) tmem_ld32_sync(o_addr + c * 32, o);
+          float f[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) f[k] = it > 0 ? __uint_as_float(o[k]) * inv : 0.f;
+          if (live) {
+            uint4* d = reinterpret_cast<uint4*>(orow + c * 32);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              d[k] = make_uint4(pack_bf16x2(f[8 * k], f[8 * k + 1]), pack_bf16x2(f[8 * k + 2], f[8 * k + 3]),
+                                pack_bf16x2(f[8 * k + 4], f[8 * k + 5]), pack_bf16x2(f[8 * k + 6], f[8 * k + 7]));
+          }
+        }
+      }
+    } else {
+      // leave the partial in this CTA's smem (the rings are free: every load was consumed by an MMA that is done
+      // once both tiles' last product is) ...
+      if (ok && it > 0) {  // both tiles' products: the other tile may still read V
+        if (has_b) ok = mbar_wait(&pv_done[1 - t], uint32_t(it - 1) & 1u, abort_flag, ZI_DEVERR_TIMEOUT_SOFTMAX);
+      }
+      float4* part = reinterpret_cast<float4*>(smem + kPart);
+      float2* ml = reinterpret_cast<float2*>(smem + kPart + 2 * 32 * 128 * 16);
+      if (ok && (t == 0 || has_b)) {
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[32];
+          if (it > 0) tmem_ld32_sync(o_addr + c * 32, o);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            part[(t * 32 + c * 8 + k) * 128 + i] =
+                it > 0 ? make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                     __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]))
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        ml[t * 128 + i] = make_float2(m_run, l);
+      }
+      __syncwarp();
+      cluster_sync();
+      // ... and join this rank's share of the columns of every row, ranks in order
+      bool bad = false;
+      for (int r = 0; r < splits; ++r)
+        bad = bad || __float_as_int(ld_cluster_f32(smem_u32(const_cast<int*>(abort_flag)), r)) != 0;
+      if (!bad && live && (t == 0 || has_b)) {
+        const uint32_t ml_addr = smem_u32(ml + t * 128 + i);
+        float w[8], mm = -INFINITY, ll = 0.f;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          w[r] = r < splits ? ld_cluster_f32(ml_addr, r) : -INFINITY;
+          mm = fmaxf(mm, w[r]);
+        }
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          w[r] = w[r] == -INFINITY ? 0.f : fast_exp2(w[r] - mm);
+          if (r < splits && w[r] != 0.f) ll = fmaf(w[r], ld_cluster_f32(ml_addr + 4, r), ll);
+        }
+        const float inv = mm == -INFINITY ? 0.f : 1.0f / ll;
+        for (int c = rank * 32 / splits; c < (rank + 1) * 32 / splits; ++c) {
+          const uint32_t addr = smem_u32(part + (t * 32 + c) * 128 + i);
+          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            if (r < splits) {
+              const float4 x = ld_cluster_f4(addr, r);
+              a = make_float4(fmaf(w[r], x.x, a.x), fmaf(w[r], x.y, a.y), fmaf(w[r], x.z, a.z), fmaf(w[r], x.w, a.w));
+            }
+          }
+          *reinterpret_cast<uint2*>(orow + 4 * c) =
+              make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+        }
+      }
+      __syncwarp();
+      cluster_sync();  // no CTA leaves while its partial may be read
+    }
+  }
+
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
 }
 
 }  // namespace zi

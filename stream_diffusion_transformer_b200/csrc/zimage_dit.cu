@@ -725,6 +725,49 @@ int run_attention_few(DevInfo* dev, const MaskedParams& p, cudaStream_t st) {
                                 few::kSmemBytes, splits, st, p, splits);
 }
 
+// 4-D map over K or V: [batch][rows][heads][128] in any strides (those of size-1 dimensions are
+// not followed: any valid value), boxes of 64 columns x 128 rows of one head, 128-byte swizzle,
+// rows past the end zero.
+int make_kv_map(CUtensorMap* m, const uint16_t* base, long long bs, long long rs, long long hs, int batch, int rows,
+                int heads) {
+  EncodeTiledFn enc;
+  if (encode_fn(&enc) != ZI_OK) return ZI_ERR_CUDA;
+  const cuuint64_t dims[4] = {128, cuuint64_t(heads), cuuint64_t(rows), cuuint64_t(batch)};
+  const cuuint64_t strides[3] = {cuuint64_t(hs ? hs * 2 : 256), cuuint64_t(rs ? rs * 2 : 256),
+                                 cuuint64_t(bs ? bs * 2 : 256)};
+  const cuuint32_t box[4] = {64, 1, 128, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t*>(base), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? ZI_OK : ZI_ERR_CUDA;
+}
+
+template <bool CAP, bool BIAS>
+int run_attention_many(DevInfo* dev, const MaskedParams& p, cudaStream_t st) {
+  CUtensorMap tk, tv;
+  ZI_TRY(make_kv_map(&tk, p.k, p.k_bs, p.k_rs, p.k_hs, p.batch, p.kv_len, p.kv_heads));
+  ZI_TRY(make_kv_map(&tv, p.v, p.v_bs, p.v_rs, p.v_hs, p.batch, p.kv_len, p.kv_heads));
+  constexpr auto kern = attention_many_kernel<CAP, BIAS>;
+  ZI_TRY((raise_smem<kern>(dev, int(many::kSmemBytes))));
+  const long long x = (static_cast<long long>(p.q_len) * p.group + 255) / 256;
+  const long long units = x * p.kv_heads * p.batch;
+  const int tiles = (p.kv_len + 127) / 128;
+  int splits = 1;
+  while (splits < 8 && units * 2 * splits <= dev->sms && 4 * splits <= tiles) splits *= 2;
+  return launch_clustered<kern>(ZI_KERNEL_ATTENTION_MASKED,
+                                dim3(unsigned(x * splits), unsigned(p.kv_heads), unsigned(p.batch)), many::kThreads,
+                                many::kSmemBytes, splits, st, tk, tv, p, splits);
+}
+
+// A step over a cache and the like (up to 16 rows per key head) is bound by reading K and V.
+int run_attention_masked(DevInfo* dev, const MaskedParams& p, cudaStream_t st) {
+  if (static_cast<long long>(p.q_len) * p.group <= 16) return run_attention_few(dev, p, st);
+  if (p.cap_log2 != 0.f)
+    return p.slopes ? run_attention_many<true, true>(dev, p, st) : run_attention_many<true, false>(dev, p, st);
+  return p.slopes ? run_attention_many<false, true>(dev, p, st) : run_attention_many<false, false>(dev, p, st);
+}
+
 // Checks one operand's strides; those of dimensions of size 1 are not read and become 0.
 int check_strides(const void* ptr, int64_t bs, int64_t rs, int64_t hs, int batch, int rows, int heads, long long* out) {
   if (!ptr) return ZI_ERR_ARG;
@@ -1024,7 +1067,7 @@ int zi_attention_masked(const zi_attention_desc* d, zi_stream_t stream) {
   p.k_doc = d->d_k_doc;
   DevInfo* dev;
   ZI_TRY(current_device(&dev));
-  return run_attention_few(dev, p, reinterpret_cast<cudaStream_t>(stream));
+  return run_attention_masked(dev, p, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int zi_fp4_scale_size(int format, int rows, int cols, size_t* h_bytes) {
