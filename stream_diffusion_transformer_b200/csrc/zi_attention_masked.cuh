@@ -18,6 +18,7 @@ struct MaskedParams {
   int batch, heads, kv_heads, group, q_len, kv_len;
   float scale_log2;     // scale * log2(e); with a cap: scale / cap
   float cap_log2;       // cap * log2(e), 0 = no cap
+  int cap_poly;         // the cap's polynomial can be used (its coefficients' powers of the scale stay in range)
   const float* slopes;  // [heads] or null
   int causal;
   const int* prefix;    // [batch] or null
@@ -357,16 +358,16 @@ constexpr uint32_t kPart = kK0;
 static_assert(kPart + 2 * 32 * 128 * 16 + 256 * 8 <= kBar, "partials fit the rings");
 }  // namespace many
 
-// tanh on [-1, 1] as z P(z^2) for a pair on the FMA pipe: a degree-9 odd polynomial fitted
-// here by the Remez exchange on the absolute error (2.8e-6 at most).  c: P's coefficients times
-// the cap, so the result is cap tanh(z).
-ZI_DEV uint64_t cap_poly_pair(uint64_t z2, const float* c) {
-  const uint64_t u = f2_mul(z2, z2);
-  uint64_t r = f2_fma(f2_pack(c[4], c[4]), u, f2_pack(c[3], c[3]));
-  r = f2_fma(r, u, f2_pack(c[2], c[2]));
+// cap tanh(z) for a pair on the FMA pipe, |z| <= 3/4: z P(z^2) with a degree-7 odd polynomial
+// fitted here by the Remez exchange on the absolute error (3.7e-6 at most).  c: its
+// coefficients times the cap and the powers of the score's factor, so s2 are raw scores.
+constexpr float kCapRange = 0.75f;
+ZI_DEV uint64_t cap_poly_pair(uint64_t s2, const float* c) {
+  const uint64_t u = f2_mul(s2, s2);
+  uint64_t r = f2_fma(f2_pack(c[3], c[3]), u, f2_pack(c[2], c[2]));
   r = f2_fma(r, u, f2_pack(c[1], c[1]));
   r = f2_fma(r, u, f2_pack(c[0], c[0]));
-  return f2_mul(r, z2);
+  return f2_mul(r, s2);
 }
 
 ZI_DEV void tma_load_4d(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z, int w) {
@@ -688,13 +689,21 @@ __global__ void __launch_bounds__(many::kThreads, 1)
     } else if (clean) {
       int it = 0;
       for (int j = first; j < my_j1; j = next(j + 1), ++it) {
-        if (!mbar_wait(&v_full[it & 1], (uint32_t(it) >> 1) & 1u, abort_flag, ZI_DEVERR_TIMEOUT_SOFTMAX)) break;
+        uint32_t dirty = 0;  // bit e: nobody sees key j 128 + e 32 + lane
         if (state(j) != 1) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int key = j * 128 + e * 32 + lane;
+            dirty |= (key >= n || (kd && __ldg(kd + key) < 0) ? 1u : 0u) << e;
+          }
+        }
+        if (!mbar_wait(&v_full[it & 1], (uint32_t(it) >> 1) & 1u, abort_flag, ZI_DEVERR_TIMEOUT_SOFTMAX)) break;
+        if (__any_sync(0xffffffffu, dirty != 0)) {
           uint8_t* v = smem + kV0 + (it & 1) * kTile;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int r = e * 32 + lane, key = j * 128 + r;
-            if (key >= n || (kd && __ldg(kd + key) < 0)) {
+            const int r = e * 32 + lane;
+            if (dirty >> e & 1u) {
 #pragma unroll
               for (int x = 0; x < 8; ++x) {
                 *reinterpret_cast<uint4*>(v + r * 128 + x * 16) = make_uint4(0, 0, 0, 0);
@@ -724,18 +733,36 @@ __global__ void __launch_bounds__(many::kThreads, 1)
     bool ok = !skip;
     int it = 0;
     if (t == 0 || has_b) {
-      const float slope = BIAS && row < rows ? __ldg(p.slopes + hk * p.group + qg) * 1.4426950408889634f : 0.f;
-      const float pos = float(qi + n - p.q_len);
-      float cc[5];
+      // scores are in the exp2 domain after a cap, and scaled into it by the exponential's argument without one
+      const float sl2 = CAP ? 1.f : p.scale_log2;
+      float slope = 0.f, pos = 0.f;
+      int pos_lo = 0, pos_hi = 0;  // places of the warp's first and last row
+      if constexpr (BIAS) {
+        const int r = min(row, rows - 1), ri = r / p.group;
+        slope = __ldg(p.slopes + hk * p.group + r - ri * p.group) * (1.4426950408889634f / sl2);
+        pos = float(ri + n - p.q_len);
+        pos_lo = __shfl_sync(0xffffffffu, ri, 0) + n - p.q_len;
+        pos_hi = __shfl_sync(0xffffffffu, ri, 31) + n - p.q_len;
+      }
+      float cc[4];
       if constexpr (CAP) {
-        cc[0] = 0.9999684695f * p.cap_log2;
-        cc[1] = -0.332658232f * p.cap_log2;
-        cc[2] = 0.1292206686f * p.cap_log2;
-        cc[3] = -0.0432998637f * p.cap_log2;
-        cc[4] = 0.008365886568f * p.cap_log2;
+        const float z1 = p.scale_log2, z2 = z1 * z1, y1 = z1 * p.cap_log2;
+        cc[0] = 0.9999556008f * y1;
+        cc[1] = -0.3322276376f * y1 * z2;
+        cc[2] = 0.1257709249f * y1 * z2 * z2;
+        cc[3] = -0.0337782849f * y1 * z2 * z2 * z2;
       }
       uint32_t s[128];
       for (int j = first; ok && j < my_j1; j = next(j + 1), ++it) {
+        const bool part = state(j) != 1;
+        int id[4];  // document ids of keys w 32 + lane, on their way while S is computed
+        if (kd && part) {
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const int key = j * 128 + w * 32 + lane;
+            id[w] = key < n ? __ldg(kd + key) : -1;
+          }
+        }
         if (!mbar_wait(&s_full[t], uint32_t(it) & 1u, abort_flag, ZI_DEVERR_TIMEOUT_SOFTMAX)) {
           ok = false;
           break;
@@ -747,19 +774,18 @@ __global__ void __launch_bounds__(many::kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) reg_fence32(&s[c * 32]);
         if constexpr (CAP) {
-          // |z| <= 1 over the warp's rows: the polynomial; else (scores past the cap) through exp and a
-          // reciprocal.  NaN (a key row that nobody sees) fails neither comparison's result: it is masked below.
-          float mx = 0.f;
+          // |z| within the polynomial's range over the warp's rows, or (scores near the cap and past it) through
+          // exp and a reciprocal.  A NaN, of a key row that nobody sees, stays in its column and is masked below.
+          float mx4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int c = 0; c < 128; c += 2)
-            mx = max3f(mx, fabsf(__uint_as_float(s[c])), fabsf(__uint_as_float(s[c + 1])));
-          const uint64_t k2 = f2_pack(p.scale_log2, p.scale_log2);
-          if (__all_sync(0xffffffffu, mx * p.scale_log2 <= 1.f)) {
+            mx4[c / 2 & 3] = max3f(mx4[c / 2 & 3], fabsf(__uint_as_float(s[c])), fabsf(__uint_as_float(s[c + 1])));
+          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+          if (p.cap_poly && __all_sync(0xffffffffu, mx * p.scale_log2 <= kCapRange)) {
 #pragma unroll
             for (int c = 0; c < 64; ++c) {
-              const uint64_t z = f2_mul(f2_pack(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), k2);
               float y0, y1;
-              f2_unpack(cap_poly_pair(z, cc), y0, y1);
+              f2_unpack(cap_poly_pair(f2_pack(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), cc), y0, y1);
               s[2 * c] = __float_as_uint(y0);
               s[2 * c + 1] = __float_as_uint(y1);
             }
@@ -769,40 +795,36 @@ __global__ void __launch_bounds__(many::kThreads, 1)
               s[c] = __float_as_uint(tanh_exp(__uint_as_float(s[c]) * p.scale_log2) * p.cap_log2);
           }
         }
+        float base = 0.f;  // what every score of the row in this tile still lacks, in the exp2 domain
         if constexpr (BIAS) {
           const float away = pos - float(j * 128);
+          const bool below = j * 128 + 127 <= pos_lo;
+          if (below || j * 128 >= pos_hi) {
+            // every key on one side of every row of the warp: |p_i - j| is linear, its row part goes to the base
+            const float sg = below ? slope : -slope;
+            base = -sg * away * sl2;
 #pragma unroll
-          for (int c = 0; c < 128; ++c) {
-            const float y = CAP ? __uint_as_float(s[c]) : __uint_as_float(s[c]) * p.scale_log2;
-            s[c] = __float_as_uint(fmaf(-slope, fabsf(away - float(c)), y));
+            for (int c = 0; c < 128; ++c) s[c] = __float_as_uint(fmaf(sg, float(c), __uint_as_float(s[c])));
+          } else {
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+              s[c] = __float_as_uint(fmaf(-slope, fabsf(away - float(c)), __uint_as_float(s[c])));
           }
         }
-        if (state(j) != 1) {
+        if (part) {
           // bit c of vis: the row sees key j 128 + c
           uint32_t vis[4];
           const int left = lim - j * 128;
 #pragma unroll
           for (int w = 0; w < 4; ++w) vis[w] = left >= 32 * w + 32 ? ~0u : left <= 32 * w ? 0u : (1u << (left - 32 * w)) - 1u;
           if (kd) {
-            int id[4];
+            for (uint32_t todo = ~0u; todo;) {  // once for each document among the warp's rows
+              const int d = __shfl_sync(0xffffffffu, doc, __ffs(todo) - 1);
+              todo &= ~__ballot_sync(0xffffffffu, doc == d);
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const int key = j * 128 + w * 32 + lane;
-              id[w] = key < n ? __ldg(kd + key) : -1;
-            }
-            const int doc0 = __shfl_sync(0xffffffffu, doc, 0);
-            if (__all_sync(0xffffffffu, doc == doc0)) {
-#pragma unroll
-              for (int w = 0; w < 4; ++w) vis[w] &= __ballot_sync(0xffffffffu, id[w] == doc0);
-            } else {
-#pragma unroll 1
-              for (int r = 0; r < 32; ++r) {
-                const int dr = __shfl_sync(0xffffffffu, doc, r);
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                  const uint32_t m = __ballot_sync(0xffffffffu, id[w] == dr);
-                  if (r == lane) vis[w] &= m;
-                }
+              for (int w = 0; w < 4; ++w) {
+                const uint32_t same = __ballot_sync(0xffffffffu, id[w] == d);
+                if (doc == d) vis[w] &= same;
               }
             }
           }
@@ -810,7 +832,6 @@ __global__ void __launch_bounds__(many::kThreads, 1)
           for (int c = 0; c < 128; ++c)
             if (!(vis[c >> 5] >> (c & 31) & 1u)) s[c] = __float_as_uint(-INFINITY);
         }
-        const float sl2 = CAP || BIAS ? 1.f : p.scale_log2;  // scores are in the exp2 domain already, or scaled on the way
         float mx8[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) mx8[k] = __uint_as_float(s[k]);
@@ -822,7 +843,7 @@ __global__ void __launch_bounds__(many::kThreads, 1)
 #pragma unroll
         for (int k = 0; k < 8; ++k) mx8[k] = fmaxf(mx8[k], __uint_as_float(s[120 + k]));
         const float mx = max3f(max3f(mx8[0], mx8[1], mx8[2]), max3f(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
-        const float m_new = fmaxf(m_run, mx * sl2);
+        const float m_new = fmaxf(m_run, fmaf(mx, sl2, base));
         // each row moves its maximum by its own scores alone, so its result does not depend on its neighbours
         const bool grows = m_new > m_run + 8.0f;
         const bool resc = __any_sync(0xffffffffu, grows);
@@ -833,16 +854,16 @@ __global__ void __launch_bounds__(many::kThreads, 1)
           l *= alpha;
         }
         const float m_use = m_run == -INFINITY ? 0.f : m_run;
-        const uint64_t sl2x2 = f2_pack(sl2, sl2), negm = f2_pack(-m_use, -m_use);
+        const uint64_t sl2x2 = f2_pack(sl2, sl2), negm = f2_pack(base - m_use, base - m_use);
         uint64_t sum2[4] = {0, 0, 0, 0};
         uint32_t pw[64];
 #pragma unroll
         for (int c = 0; c < 64; ++c) {
           float x0, x1;
           const uint64_t s2 = f2_pack(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]));
-          f2_unpack(CAP || BIAS ? f2_add(s2, negm) : f2_fma(s2, sl2x2, negm), x0, x1);
+          f2_unpack(CAP ? f2_add(s2, negm) : f2_fma(s2, sl2x2, negm), x0, x1);
           float e0, e1;
-          if ((c & 7) == 1 || (c & 7) == 4 || (c & 7) == 6) {  // 3 of 8 pairs on the FMA pipe
+          if (!CAP && ((c & 7) == 1 || (c & 7) == 4 || (c & 7) == 6)) {  // 3 of 8 pairs on the FMA pipe; the cap fills it
             exp2_poly_pair(x0, x1, e0, e1);
           } else {
             e0 = fast_exp2(x0);

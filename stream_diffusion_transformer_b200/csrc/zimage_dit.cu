@@ -1059,6 +1059,7 @@ int zi_attention_masked(const zi_attention_desc* d, zi_stream_t stream) {
   const double log2e = 1.4426950408889634;
   p.scale_log2 = d->softcap > 0.f ? float(double(d->scale) / d->softcap) : float(double(d->scale) * log2e);
   p.cap_log2 = float(double(d->softcap) * log2e);
+  p.cap_poly = p.scale_log2 > 1e-4f && p.scale_log2 < 1e4f && p.cap_log2 > 1e-3f && p.cap_log2 < 1e6f;
   p.slopes = d->d_slopes;
   p.causal = d->causal;
   p.prefix = d->d_prefix_len;
