@@ -12,6 +12,7 @@
 #include <cuda_fp4.h>
 
 #include "zi_common.cuh"
+#include "zi_gemm.cuh"
 
 namespace zi {
 namespace fp4 {
@@ -545,6 +546,254 @@ __global__ void __launch_bounds__(kNarrowThreads)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, L::kCols);
+  }
+}
+
+// ------------------------------------------------------------------ product: many rows
+// CTA pairs (cta_group::2) on 256 x 256 tiles, as gemm_pair_body: each CTA stages its own 128
+// rows of A and of B (128 bytes, 256 columns, of K per stage) and the block scales that its
+// tensor core needs, A's for its own rows and B's for all 256 columns; CTA 0 issues
+// M = 256 MMAs for both SMs after copying the scales to TMEM.  TMEM holds one accumulator
+// (256 columns): the scale columns leave no room for a second, so the epilogue warps take
+// the whole accumulator into registers (128 columns each) and hand it back before they
+// scale and store, and the MMAs of the next tile wait for the TMEM reads alone.
+// Warps: 0 loads, 1 MMA, 2..9 epilogue.
+constexpr int kWideThreads = 320;
+
+template <int FMT>
+struct WideSmem {
+  static constexpr uint32_t kA = 128 * 128, kB = 128 * 128;
+  static constexpr uint32_t kSc = kStageTiles<FMT> * kTileBytes;  // 128 rows of scales
+  static constexpr uint32_t kStage = kA + kB + 3 * kSc;
+  static constexpr int kStages = FMT == MX ? 6 : 5;
+  static constexpr uint32_t kBar = kStages * kStage;
+  static constexpr uint32_t kBytes = kBar + 256 + 1024;
+  static constexpr uint32_t kColScale = 256;
+  static constexpr uint32_t kScaleCols = 12 * kStageTiles<FMT>;  // A's 4 and B's 8 columns per scale tile
+  static_assert(kStage % 1024 == 0 && kBytes <= 232448, "stage alignment, shared memory");
+  static_assert(kColScale + 2 * kScaleCols <= 512, "TMEM columns");
+};
+
+ZI_DEV void load_3d_pair(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+      "[%2];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(leader_addr(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// As mma and copy_scales, over the pair: each CTA's scales go from its own smem to its own TMEM.
+template <int FMT>
+ZI_DEV void mma2(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sa_tmem, uint32_t sb_tmem,
+                 uint32_t accumulate) {
+  if constexpr (FMT == MX) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sa_tmem), "r"(sb_tmem)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sa_tmem), "r"(sb_tmem)
+        : "memory");
+  }
+}
+ZI_DEV void copy_scales2(uint32_t tmem_col, uint32_t saddr) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem_col), "l"(scale_desc(saddr)) : "memory");
+}
+
+template <int FMT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
+    gemm_wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                     const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB, GemmParams p,
+                     TailSched sched) {
+  using L = WideSmem<FMT>;
+  constexpr int kStages = L::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar);  // CTA 0: both CTAs' stage loaded
+  uint64_t* empty = full + kStages;   // each CTA: its stage consumed
+  uint64_t* tfull = empty + kStages;  // each CTA: accumulator complete
+  uint64_t* tempty = tfull + 1;       // CTA 0: both CTAs' epilogues hold the accumulator
+  uint64_t* drain = tempty + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int unit = blockIdx.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(tfull, 1);
+    mbar_init(tempty, 16);  // one arrival per epilogue warp of each CTA
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmB);
+    prefetch_tmap(&tmSA);
+    prefetch_tmap(&tmSB);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers initialised and TMEM allocated before any remote access
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const bool err = device_error_set();  // an earlier kernel timed out: skip the work, still meet at the end
+  const int num_m = (p.M + 255) / 256;
+  WorkItem wi;
+
+  if (err) {
+  } else if (warp == 0) {
+    if (lane == 0) {
+      uint32_t it = 0;
+      bool ok = true;
+      WorkWalker walk(sched, unit);
+      while (ok && walk.next(wi)) {
+        int m0, n0;
+        tile_origin<256, 256>(sched, num_m, wi.tile, m0, n0);
+        for (int kb = 0; kb < sched.kb; ++kb, ++it) {
+          const uint32_t s = it % kStages, r = it / kStages;
+          if (!mbar_wait(&empty[s], (r & 1u) ^ 1u, abort_flag, ZI_DEVERR_TIMEOUT_PRODUCER)) {
+            ok = false;
+            break;
+          }
+          uint8_t* st = smem + s * L::kStage;
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2u * L::kStage);
+          tma_load_2d_pair(st, &tmA, &full[s], kb * 128, m0 + 128 * int(rank));
+          tma_load_2d_pair(st + L::kA, &tmB, &full[s], kb * 128, n0 + 128 * int(rank));
+          uint8_t* sc = st + L::kA + L::kB;
+          load_3d_pair(sc, &tmSA, &full[s], 0, kb * kStageTiles<FMT>, m0 / 128 + int(rank));
+          load_3d_pair(sc + L::kSc, &tmSB, &full[s], 0, kb * kStageTiles<FMT>, n0 / 128);
+          load_3d_pair(sc + 2 * L::kSc, &tmSB, &full[s], 0, kb * kStageTiles<FMT>, n0 / 128 + 1);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      uint32_t it = 0;
+      int local = 0;
+      bool ok = true;
+      WorkWalker walk(sched, unit);
+      while (ok && walk.next(wi)) {
+        if (!mbar_wait(tempty, (uint32_t(local) & 1u) ^ 1u, abort_flag, ZI_DEVERR_TIMEOUT_MMA)) {
+          ok = false;
+          break;
+        }
+        ++local;
+        tc_fence_after();
+        for (int kb = 0; kb < sched.kb; ++kb, ++it) {
+          const uint32_t s = it % kStages, r = it / kStages;
+          if (!mbar_wait(&full[s], r & 1u, abort_flag, ZI_DEVERR_TIMEOUT_MMA)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a_addr = smem_u32(smem + s * L::kStage), b_addr = a_addr + L::kA, sc = b_addr + L::kB;
+          const uint32_t tsa = tmem + L::kColScale + (it & 1) * L::kScaleCols, tsb = tsa + 4 * kStageTiles<FMT>;
+#pragma unroll
+          for (int t = 0; t < kStageTiles<FMT>; ++t) {
+            copy_scales2(tsa + 4 * t, sc + t * kTileBytes);
+            copy_scales2(tsb + 8 * t, sc + L::kSc + t * kTileBytes);
+            copy_scales2(tsb + 8 * t + 4, sc + 2 * L::kSc + t * kTileBytes);
+          }
+          // columns past K are zero codes under zero scales: whole steps of 64 past it are left out
+          const int ksteps = min(4, (p.K - kb * kStageK + 63) / 64);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (k < ksteps) {
+              const int t = FMT == MX ? k >> 1 : k;
+              mma2<FMT>(tmem, smem_desc_sw128(a_addr + k * 32, 16), smem_desc_sw128(b_addr + k * 32, 16),
+                        idesc<FMT>(256, 256, FMT == MX ? k & 1 : 0), tsa + 4 * t, tsb + 8 * t,
+                        (kb | k) != 0 ? 1u : 0u);
+            }
+          }
+          tc_commit_pair(&empty[s]);
+        }
+        if (ok) tc_commit_pair(tfull);
+      }
+      if (!ok) {
+        tc_commit_pair_local(drain);
+        volatile int never = 0;
+        mbar_wait(drain, 0, &never, ZI_DEVERR_TIMEOUT_DRAIN);
+      }
+    }
+  } else {
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    int local = 0;
+    WorkWalker walk(sched, unit);
+    while (walk.next(wi)) {
+      if (!mbar_wait(tfull, uint32_t(local) & 1u, abort_flag, ZI_DEVERR_TIMEOUT_EPILOGUE)) break;
+      ++local;
+      tc_fence_after();
+      uint32_t v[128];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(tmem + (uint32_t(q * 32) << 16) + half * 128 + c * 32, &v[c * 32]);
+      tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) reg_fence32(&v[c * 32]);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_leader(tempty);
+      int m0, n0;
+      tile_origin<256, 256>(sched, num_m, wi.tile, m0, n0);
+      const int m = m0 + 128 * int(rank) + q * 32 + lane, nb = n0 + half * 128;
+      if (m < p.M) {
+        const float ra = FMT == NV ? __ldg(p.ars + m) : 1.f;
+        uint16_t* out = p.out + size_t(m) * p.N + nb;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {  // 8 columns; N is a multiple of 8
+          if (nb + 8 * c < p.N) {
+            float f[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[8 * c + i]);
+            if constexpr (FMT == NV) {
+              const float4* bs = reinterpret_cast<const float4*>(p.brs + nb + 8 * c);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const float4 w = __ldg(bs + h);
+                f[4 * h] *= ra * w.x;
+                f[4 * h + 1] *= ra * w.y;
+                f[4 * h + 2] *= ra * w.z;
+                f[4 * h + 3] *= ra * w.w;
+              }
+            }
+            *reinterpret_cast<uint4*>(out + 8 * c) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                                                                pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+          }
+        }
+      }
+    }
+  }
+
+  if (*abort_flag) {  // an aborted pipeline: let copies already issued land before the pair leaves
+    const unsigned long long t0 = globaltimer();
+    while (globaltimer() - t0 < 200000ull) {
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // neither CTA frees TMEM or exits while the pair's MMAs or copies may use it
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
   }
 }
 

@@ -701,12 +701,53 @@ int run_fp4_narrow(DevInfo* dev, const uint8_t* a, const uint8_t* b, const fp4::
                                 L::kBytes, splits, st, ta, tb, p, splits);
 }
 
+// 3-D map over block scales: [rows of tiles][tiles along][128 words]; boxes of one stage's tiles of 128
+// rows, tiles outside the matrix zero.
+int make_scale_map(CUtensorMap* m, const uint8_t* base, int tiles_x, int tiles_y, int box_tiles) {
+  EncodeTiledFn enc;
+  if (encode_fn(&enc) != ZI_OK) return ZI_ERR_CUDA;
+  const cuuint64_t dims[3] = {128, cuuint64_t(tiles_x), cuuint64_t(tiles_y)};
+  const cuuint64_t strides[2] = {fp4::kTileBytes, cuuint64_t(tiles_x) * fp4::kTileBytes};
+  const cuuint32_t box[3] = {128, cuuint32_t(box_tiles), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<uint8_t*>(base), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? ZI_OK : ZI_ERR_CUDA;
+}
+
+template <int FMT>
+int run_fp4_wide(DevInfo* dev, const uint8_t* a, const uint8_t* b, const fp4::GemmParams& p, cudaStream_t st) {
+  using L = fp4::WideSmem<FMT>;
+  if (dev->sms < 2) return ZI_ERR_DEVICE;
+  CUtensorMap ta, tb, tsa, tsb;
+  ZI_TRY(make_map(&ta, a, uint64_t(p.K / 2), uint64_t(p.M), uint64_t(p.K / 2), 128, 128, CU_TENSOR_MAP_DATA_TYPE_UINT8));
+  ZI_TRY(make_map(&tb, b, uint64_t(p.K / 2), uint64_t(p.N), uint64_t(p.K / 2), 128, 128, CU_TENSOR_MAP_DATA_TYPE_UINT8));
+  const int tx = fp4::tiles_along<FMT>(p.K);
+  ZI_TRY(make_scale_map(&tsa, p.abs, tx, fp4::tiles_down(p.M), fp4::kStageTiles<FMT>));
+  ZI_TRY(make_scale_map(&tsb, p.bbs, tx, fp4::tiles_down(p.N), fp4::kStageTiles<FMT>));
+  constexpr auto kern = fp4::gemm_wide_kernel<FMT>;
+  ZI_TRY((raise_smem<kern>(dev, int(L::kBytes))));
+  const int num_m = (p.M + 255) / 256, num_n = (p.N + 255) / 256;
+  const long long tiles = static_cast<long long>(num_m) * num_n;
+  if (tiles > 0x7fffffffLL - kMaxDim) return ZI_ERR_SHAPE;
+  const double panel = 256.0 * (p.K / 2 + p.K / fp4::kBlock<FMT>);
+  int group, group_n;
+  choose_raster(num_m, num_n, panel, panel, group, group_n);
+  const TailSched sched = make_tail_sched(int(tiles), dev->sms / 2, (p.K + fp4::kStageK - 1) / fp4::kStageK, false, num_n,
+                                          group, group_n);
+  prof_pre(st);
+  kern<<<2 * sched_units(sched, int(tiles)), fp4::kWideThreads, L::kBytes, st>>>(ta, tb, tsa, tsb, p, sched);
+  return launched(ZI_KERNEL_GEMM_FP4, st);
+}
+
 template <int FMT>
 int run_fp4_gemm(DevInfo* dev, const uint8_t* a, const uint8_t* b, const fp4::GemmParams& p, cudaStream_t st) {
   if (p.M <= 16) return run_fp4_narrow<FMT, 16>(dev, a, b, p, st);
   if (p.M <= 32) return run_fp4_narrow<FMT, 32>(dev, a, b, p, st);
   if (p.M <= 64) return run_fp4_narrow<FMT, 64>(dev, a, b, p, st);
-  return run_fp4_narrow<FMT, 128>(dev, a, b, p, st);
+  if (p.M <= 512) return run_fp4_narrow<FMT, 128>(dev, a, b, p, st);
+  return run_fp4_wide<FMT>(dev, a, b, p, st);
 }
 
 // ---------------------------------------------------------------- masked attention
