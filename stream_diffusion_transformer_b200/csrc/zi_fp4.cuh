@@ -553,12 +553,19 @@ __global__ void __launch_bounds__(kNarrowThreads)
 // CTA pairs (cta_group::2) on 256 x 256 tiles, as gemm_pair_body: each CTA stages its own 128
 // rows of A and of B (128 bytes, 256 columns, of K per stage) and the block scales that its
 // tensor core needs, A's for its own rows and B's for all 256 columns; CTA 0 issues
-// M = 256 MMAs for both SMs after copying the scales to TMEM.  TMEM holds one accumulator
-// (256 columns): the scale columns leave no room for a second, so the epilogue warps take
-// the whole accumulator into registers (128 columns each) and hand it back before they
-// scale and store, and the MMAs of the next tile wait for the TMEM reads alone.
-// Warps: 0 loads, 1 MMA, 2..9 epilogue.
-constexpr int kWideThreads = 320;
+// M = 256 MMAs for both SMs.
+// - Scales reach TMEM through registers: four warps, one per lane quarter, read a stage's
+//   scale tiles from smem and store them with tcgen05.st while earlier MMAs run.  tcgen05.cp
+//   would do it in the tensor core's own queue, where each 512-byte tile took about 55 cycles
+//   between the MMAs (4128 x 20480 x 3840 NVFP4: 252 us with it).
+// - TMEM holds one accumulator (256 columns) and one scale buffer per smem stage; there is no
+//   room for a second accumulator, so the epilogue warps take the whole accumulator into
+//   registers (128 columns each) and hand it back before they scale and store: the MMAs of
+//   the next tile wait for the TMEM reads alone.
+// Warps: 0 loads, 1 MMA, 2..3 idle, 4..7 scales, 8..15 epilogue; registers move from the
+// first two warpgroups to the epilogue (128 a thread at launch; 56 + 64 + 2 x 192 = 504 <= 512).
+constexpr int kWideThreads = 512;
+constexpr int kWideRegsLow = 56, kWideRegsScale = 64, kWideRegsEpi = 192;
 
 template <int FMT>
 struct WideSmem {
@@ -571,18 +578,18 @@ struct WideSmem {
   static constexpr uint32_t kColScale = 256;
   static constexpr uint32_t kScaleCols = 12 * kStageTiles<FMT>;  // A's 4 and B's 8 columns per scale tile
   static_assert(kStage % 1024 == 0 && kBytes <= 232448, "stage alignment, shared memory");
-  static_assert(kColScale + 2 * kScaleCols <= 512, "TMEM columns");
+  static_assert(kColScale + kStages * kScaleCols <= 512, "TMEM columns");
 };
 
-ZI_DEV void load_3d_pair(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
+ZI_DEV void load_3d(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
-      "[%2];" ::"r"(smem_u32(smem_dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(leader_addr(bar)), "r"(x), "r"(y), "r"(z)
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+          smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
 
-// As mma and copy_scales, over the pair: each CTA's scales go from its own smem to its own TMEM.
+// As mma, over the pair: each CTA's scales come from its own TMEM.
 template <int FMT>
 ZI_DEV void mma2(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sa_tmem, uint32_t sb_tmem,
                  uint32_t accumulate) {
@@ -604,8 +611,12 @@ ZI_DEV void mma2(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc
         : "memory");
   }
 }
-ZI_DEV void copy_scales2(uint32_t tmem_col, uint32_t saddr) {
-  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem_col), "l"(scale_desc(saddr)) : "memory");
+
+// 4 consecutive columns of this warp's 32 lanes.
+ZI_DEV void tmem_st4(uint32_t taddr, uint4 w) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(w.x), "r"(w.y),
+               "r"(w.z), "r"(w.w)
+               : "memory");
 }
 
 template <int FMT>
@@ -617,10 +628,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
   constexpr int kStages = L::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar);  // CTA 0: both CTAs' stage loaded
-  uint64_t* empty = full + kStages;   // each CTA: its stage consumed
-  uint64_t* tfull = empty + kStages;  // each CTA: accumulator complete
-  uint64_t* tempty = tfull + 1;       // CTA 0: both CTAs' epilogues hold the accumulator
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar);  // CTA 0: both CTAs' operands loaded
+  uint64_t* empty = full + kStages;     // each CTA: its stage consumed by the pair's MMAs
+  uint64_t* sc_full = empty + kStages;  // each CTA: its scales loaded
+  uint64_t* sc_tmem = sc_full + kStages;  // CTA 0: both CTAs' scales in TMEM
+  uint64_t* tfull = sc_tmem + kStages;  // each CTA: accumulator complete
+  uint64_t* tempty = tfull + 1;         // CTA 0: both CTAs' epilogues hold the accumulator
   uint64_t* drain = tempty + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -633,6 +646,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
+      mbar_init(&sc_full[s], 1);
+      mbar_init(&sc_tmem[s], 8);  // one arrival per scale warp of each CTA
     }
     mbar_init(tfull, 1);
     mbar_init(tempty, 16);  // one arrival per epilogue warp of each CTA
@@ -660,9 +675,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
   const int num_m = (p.M + 255) / 256;
   WorkItem wi;
 
-  if (err) {
-  } else if (warp == 0) {
-    if (lane == 0) {
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWideRegsLow));
+    if (warp == 0 && lane == 0 && !err) {
       uint32_t it = 0;
       bool ok = true;
       WorkWalker walk(sched, unit);
@@ -676,18 +691,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
             break;
           }
           uint8_t* st = smem + s * L::kStage;
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2u * L::kStage);
+          uint8_t* sc = st + L::kA + L::kB;
+          mbar_arrive_expect_tx(&sc_full[s], 3u * L::kSc);
+          load_3d(sc, &tmSA, &sc_full[s], 0, kb * kStageTiles<FMT>, m0 / 128 + int(rank));
+          load_3d(sc + L::kSc, &tmSB, &sc_full[s], 0, kb * kStageTiles<FMT>, n0 / 128);
+          load_3d(sc + 2 * L::kSc, &tmSB, &sc_full[s], 0, kb * kStageTiles<FMT>, n0 / 128 + 1);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2u * (L::kA + L::kB));
           tma_load_2d_pair(st, &tmA, &full[s], kb * 128, m0 + 128 * int(rank));
           tma_load_2d_pair(st + L::kA, &tmB, &full[s], kb * 128, n0 + 128 * int(rank));
-          uint8_t* sc = st + L::kA + L::kB;
-          load_3d_pair(sc, &tmSA, &full[s], 0, kb * kStageTiles<FMT>, m0 / 128 + int(rank));
-          load_3d_pair(sc + L::kSc, &tmSB, &full[s], 0, kb * kStageTiles<FMT>, n0 / 128);
-          load_3d_pair(sc + 2 * L::kSc, &tmSB, &full[s], 0, kb * kStageTiles<FMT>, n0 / 128 + 1);
         }
       }
-    }
-  } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    } else if (warp == 1 && lane == 0 && rank == 0 && !err) {
       uint32_t it = 0;
       int local = 0;
       bool ok = true;
@@ -701,19 +715,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
         tc_fence_after();
         for (int kb = 0; kb < sched.kb; ++kb, ++it) {
           const uint32_t s = it % kStages, r = it / kStages;
-          if (!mbar_wait(&full[s], r & 1u, abort_flag, ZI_DEVERR_TIMEOUT_MMA)) {
+          if (!mbar_wait(&full[s], r & 1u, abort_flag, ZI_DEVERR_TIMEOUT_MMA) ||
+              !mbar_wait(&sc_tmem[s], r & 1u, abort_flag, ZI_DEVERR_TIMEOUT_MMA)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a_addr = smem_u32(smem + s * L::kStage), b_addr = a_addr + L::kA, sc = b_addr + L::kB;
-          const uint32_t tsa = tmem + L::kColScale + (it & 1) * L::kScaleCols, tsb = tsa + 4 * kStageTiles<FMT>;
-#pragma unroll
-          for (int t = 0; t < kStageTiles<FMT>; ++t) {
-            copy_scales2(tsa + 4 * t, sc + t * kTileBytes);
-            copy_scales2(tsb + 8 * t, sc + L::kSc + t * kTileBytes);
-            copy_scales2(tsb + 8 * t + 4, sc + 2 * L::kSc + t * kTileBytes);
-          }
+          const uint32_t a_addr = smem_u32(smem + s * L::kStage), b_addr = a_addr + L::kA;
+          const uint32_t tsa = tmem + L::kColScale + s * L::kScaleCols, tsb = tsa + 4 * kStageTiles<FMT>;
           // columns past K are zero codes under zero scales: whole steps of 64 past it are left out
           const int ksteps = min(4, (p.K - kb * kStageK + 63) / 64);
 #pragma unroll
@@ -735,11 +744,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
         mbar_wait(drain, 0, &never, ZI_DEVERR_TIMEOUT_DRAIN);
       }
     }
+    __syncwarp();
+  } else if (warp < 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWideRegsScale));
+    // Scale tiles of a stage to this warp's lane quarter: lane l of a tile's 4 columns holds rows l, 32 + l, 64 + l
+    // and 96 + l, in every quarter.  The TMEM buffer of a stage is free whenever its smem is.
+    const uint32_t quarter = uint32_t((warp & 3) * 32) << 16;
+    uint32_t it = 0;
+    bool ok = !err;
+    WorkWalker walk(sched, unit);
+    while (ok && walk.next(wi)) {
+      for (int kb = 0; kb < sched.kb; ++kb, ++it) {
+        const uint32_t s = it % kStages, r = it / kStages;
+        if (!mbar_wait(&sc_full[s], r & 1u, abort_flag, ZI_DEVERR_TIMEOUT_EPILOGUE)) {
+          ok = false;
+          break;
+        }
+        const uint4* src = reinterpret_cast<const uint4*>(smem + s * L::kStage + L::kA + L::kB) + lane;
+        const uint32_t dst = tmem + quarter + L::kColScale + s * L::kScaleCols;
+        uint4 w[3 * kStageTiles<FMT>];
+#pragma unroll
+        for (int t = 0; t < 3 * kStageTiles<FMT>; ++t) w[t] = src[t * 32];
+#pragma unroll
+        for (int t = 0; t < kStageTiles<FMT>; ++t) {
+          tmem_st4(dst + 4 * t, w[t]);
+          tmem_st4(dst + 4 * kStageTiles<FMT> + 8 * t, w[kStageTiles<FMT> + t]);
+          tmem_st4(dst + 4 * kStageTiles<FMT> + 8 * t + 4, w[2 * kStageTiles<FMT> + t]);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_leader(&sc_tmem[s]);
+      }
+    }
   } else {
-    const int q = warp & 3, half = (warp - 2) >> 2;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWideRegsEpi));
+    const int q = warp & 3, half = (warp - 8) >> 2;
     int local = 0;
     WorkWalker walk(sched, unit);
-    while (walk.next(wi)) {
+    while (!err && walk.next(wi)) {
       if (!mbar_wait(tfull, uint32_t(local) & 1u, abort_flag, ZI_DEVERR_TIMEOUT_EPILOGUE)) break;
       ++local;
       tc_fence_after();
