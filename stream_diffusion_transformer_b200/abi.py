@@ -137,7 +137,9 @@ def _check(fn: str, status: int) -> None:
 
 def call(fn: str, *args) -> None:
     """Call a status-returning entry point and raise on error."""
-    _check(fn, getattr(lib(), fn)(*args))
+    status = getattr(_lib or lib(), fn)(*args)
+    if status != ZI_OK:
+        _check(fn, status)
 
 
 def config_default() -> ZiConfig:

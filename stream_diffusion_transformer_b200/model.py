@@ -425,43 +425,65 @@ class Fp4Matrix(NamedTuple):
 _FP4_FORMATS = {"mxfp4": abi.ZI_FP4_MX, "nvfp4": abi.ZI_FP4_NV}
 
 
+def _launch(device: int, fn: str, *args) -> None:
+    """abi.call with the current stream of GPU `device` as its last argument, and that GPU current.  A few
+    microseconds of host time are as long as the smallest kernels here, so the common case (the GPU is
+    current already) enters no context and builds no stream object."""
+    if torch.cuda.current_device() == device:
+        abi.call(fn, *args, torch._C._cuda_getCurrentRawStream(device))
+    else:
+        with torch.cuda.device(device):
+            abi.call(fn, *args, torch._C._cuda_getCurrentRawStream(device))
+
+
+def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
 def _fp4_format(fmt: str) -> int:
-    if fmt not in _FP4_FORMATS:
+    f = _FP4_FORMATS.get(fmt)
+    if f is None:
         raise ValueError(f"unknown 4-bit format {fmt!r}: one of {sorted(_FP4_FORMATS)}")
-    return _FP4_FORMATS[fmt]
+    return f
+
+
+def _fp4_scale_bytes(f: int, rows: int, cols: int) -> int:
+    """zi_fp4_scale_size without the call: 512 bytes for 128 rows x 4 blocks."""
+    per = 128 if f == abi.ZI_FP4_MX else 64
+    return -(-rows // 128) * -(-cols // per) * 512
 
 
 def _fp4_check(m: Fp4Matrix) -> int:
     """The library's number of m's format, after checking m's tensors (the library sees pointers only)."""
     f = _fp4_format(m.fmt)
-    rows, cols = m.shape
-    parts = [("codes", m.codes, torch.uint8, None), ("block_scales", m.block_scales, torch.uint8,
-                                                     abi.fp4_scale_size(f, rows, cols))]
-    if (m.row_scales is not None) != (f == abi.ZI_FP4_NV):
+    q, bs, rs = m.codes, m.block_scales, m.row_scales
+    if q.dim() != 2 or q.dtype != torch.uint8 or not q.is_cuda or not q.is_contiguous():
+        raise ValueError("codes: a contiguous 2-D uint8 tensor on a GPU is needed")
+    rows, device = q.shape[0], q.get_device()
+    n = _fp4_scale_bytes(f, rows, 2 * q.shape[1])
+    if bs.dtype != torch.uint8 or not bs.is_contiguous() or bs.get_device() != device or bs.numel() != n:
+        raise ValueError(f"block_scales: a contiguous uint8 tensor of {n} elements on the codes' GPU is needed")
+    if (rs is not None) != (f == abi.ZI_FP4_NV):
         raise ValueError("row_scales belong to nvfp4 and to nvfp4 alone")
-    if f == abi.ZI_FP4_NV:
-        parts.append(("row_scales", m.row_scales, torch.float32, rows))
-    for name, t, dtype, n in parts:
-        if t.dtype != dtype or not t.is_contiguous() or t.device != m.codes.device or not t.is_cuda:
-            raise ValueError(f"{name}: a contiguous {dtype} tensor on the matrix's GPU is needed")
-        if n is not None and t.numel() != n:
-            raise ValueError(f"{name}: {t.numel()} elements, {n} are needed for {rows} x {cols} in {m.fmt}")
+    if rs is not None and (rs.dtype != torch.float32 or not rs.is_contiguous() or rs.get_device() != device
+                           or rs.numel() != rows):
+        raise ValueError(f"row_scales: a contiguous fp32 tensor of {rows} elements on the codes' GPU is needed")
     return f
 
 
 def quantize_fp4(x: torch.Tensor, fmt: str = "nvfp4") -> Fp4Matrix:
     """The rows of a 2-D fp32 or bf16 tensor in 4 bits (zi_quantize_fp4)."""
     f = _fp4_format(fmt)
-    if x.dim() != 2 or not x.is_cuda or not x.is_contiguous() or x.dtype not in (torch.float32, torch.bfloat16):
+    bf16 = x.dtype == torch.bfloat16
+    if x.dim() != 2 or not x.is_cuda or not x.is_contiguous() or not (bf16 or x.dtype == torch.float32):
         raise ValueError("quantize_fp4: a contiguous 2-D fp32 or bf16 tensor on a GPU is needed")
     rows, cols = x.shape
-    with torch.cuda.device(x.device):
-        q = torch.empty((rows, cols // 2), dtype=torch.uint8, device=x.device)
-        bs = torch.empty(abi.fp4_scale_size(f, rows, cols), dtype=torch.uint8, device=x.device)
-        rs = torch.empty(rows, dtype=torch.float32, device=x.device) if f == abi.ZI_FP4_NV else None
-        if rows:
-            abi.call("zi_quantize_fp4", f, _p(x), 1 if x.dtype == torch.bfloat16 else 0, rows, cols, _p(q), _p(bs),
-                     _p(rs), _stream())
+    q = x.new_empty((rows, cols // 2), dtype=torch.uint8)
+    bs = x.new_empty(_fp4_scale_bytes(f, rows, cols), dtype=torch.uint8)
+    rs = x.new_empty(rows, dtype=torch.float32) if f == abi.ZI_FP4_NV else None
+    if rows:
+        _launch(x.get_device(), "zi_quantize_fp4", f, x.data_ptr(), 1 if bf16 else 0, rows, cols, q.data_ptr(),
+                bs.data_ptr(), _ptr(rs))
     return Fp4Matrix(fmt, q, bs, rs)
 
 
@@ -471,29 +493,28 @@ def dequantize_fp4(m: Fp4Matrix, dtype: torch.dtype = torch.bfloat16) -> torch.T
     if dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("dequantize_fp4: fp32 or bf16")
     rows, cols = m.shape
-    with torch.cuda.device(m.codes.device):
-        y = torch.empty((rows, cols), dtype=dtype, device=m.codes.device)
-        if rows:
-            abi.call("zi_dequantize_fp4", f, _p(m.codes), _p(m.block_scales), _p(m.row_scales), rows, cols, _p(y),
-                     1 if dtype == torch.bfloat16 else 0, _stream())
+    y = m.codes.new_empty((rows, cols), dtype=dtype)
+    if rows:
+        _launch(y.get_device(), "zi_dequantize_fp4", f, m.codes.data_ptr(), m.block_scales.data_ptr(),
+                _ptr(m.row_scales), rows, cols, y.data_ptr(), 1 if dtype == torch.bfloat16 else 0)
     return y
 
 
 def gemm_fp4(a: Fp4Matrix, b: Fp4Matrix, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """bf16 [M, N] = a [M, K] b [N, K]^T of two 4-bit matrices of one format (zi_gemm_fp4)."""
     f = _fp4_check(a)
-    if _fp4_check(b) != f or a.shape[1] != b.shape[1] or a.codes.device != b.codes.device:
+    (M, K), (N, Kb) = a.shape, b.shape
+    device = a.codes.get_device()
+    if _fp4_check(b) != f or K != Kb or b.codes.get_device() != device:
         raise ValueError("gemm_fp4: two matrices of one format, one K and one device are needed")
-    (M, K), N = a.shape, b.shape[0]
-    with torch.cuda.device(a.codes.device):
-        if out is None:
-            out = torch.empty((M, N), dtype=torch.bfloat16, device=a.codes.device)
-        elif (tuple(out.shape) != (M, N) or out.dtype != torch.bfloat16 or not out.is_contiguous()
-              or out.device != a.codes.device):
-            raise ValueError("gemm_fp4: out has to be a contiguous bf16 [M, N] tensor on the operands' GPU")
-        if M:
-            abi.call("zi_gemm_fp4", f, _p(a.codes), _p(a.block_scales), _p(a.row_scales), _p(b.codes),
-                     _p(b.block_scales), _p(b.row_scales), _p(out), M, N, K, _stream())
+    if out is None:
+        out = a.codes.new_empty((M, N), dtype=torch.bfloat16)
+    elif (tuple(out.shape) != (M, N) or out.dtype != torch.bfloat16 or not out.is_contiguous()
+          or out.get_device() != device):
+        raise ValueError("gemm_fp4: out has to be a contiguous bf16 [M, N] tensor on the operands' GPU")
+    if M:
+        _launch(device, "zi_gemm_fp4", f, a.codes.data_ptr(), a.block_scales.data_ptr(), _ptr(a.row_scales),
+                b.codes.data_ptr(), b.block_scales.data_ptr(), _ptr(b.row_scales), out.data_ptr(), M, N, K)
     return out
 
 
@@ -510,31 +531,29 @@ def attention_masked(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, scale
     if q.dim() != 4 or k.dim() != 4 or k.shape != v.shape or q.shape[0] != k.shape[0] or q.shape[3] != 128 \
             or k.shape[3] != 128:
         raise ValueError("attention_masked: q [B, q_len, H, 128] and k, v [B, kv_len, Hk, 128] are needed")
-    B, n, H, _ = q.shape
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        out = q.new_empty(q.shape)
     elif out.shape != q.shape:
         raise ValueError("attention_masked: out has to have q's shape")
-    d = abi.attention_desc_init()
+    B, n, H, _ = q.shape
+    m, Hk = k.shape[1], k.shape[2]
+    device = q.get_device()
+    strides = []
     for name, t in (("q", q), ("k", k), ("v", v), ("out", out)):
-        if t.dtype != torch.bfloat16 or not t.is_cuda or t.device != q.device or t.stride(3) != 1:
+        st = t.stride()
+        if t.dtype != torch.bfloat16 or not t.is_cuda or t.get_device() != device or st[3] != 1:
             raise ValueError(f"attention_masked: {name} has to be bf16 with contiguous heads on q's GPU")
-        setattr(d, name, t.data_ptr())
-        for i, dim in enumerate(("batch", "row", "head")):
-            setattr(d, f"{name}_{dim}_stride", t.stride(i))
-    d.batch, d.heads, d.kv_heads, d.q_len, d.kv_len = B, H, k.shape[2], n, k.shape[1]
-    if scale is not None:
-        d.scale = float(scale)
-    d.softcap, d.causal = float(softcap), 1 if causal else 0
+        strides += st[:3]
     for name, t, dtype, shape in (("slopes", slopes, torch.float32, (H,)), ("prefix_len", prefix_len, torch.int32, (B,)),
                                   ("kv_len", kv_len, torch.int32, (B,)), ("q_doc", q_doc, torch.int32, (B, n)),
-                                  ("k_doc", k_doc, torch.int32, (B, k.shape[1]))):
-        if t is not None:
-            if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != q.device:
-                raise ValueError(f"attention_masked: {name} has to be a contiguous {dtype} tensor {shape} on q's GPU")
-            setattr(d, f"d_{name}", t.data_ptr())
-    with torch.cuda.device(q.device):
-        abi.call("zi_attention_masked", ctypes.byref(d), _stream())
+                                  ("k_doc", k_doc, torch.int32, (B, m))):
+        if t is not None and (t.dtype != dtype or t.shape != shape or not t.is_contiguous()
+                              or t.get_device() != device):
+            raise ValueError(f"attention_masked: {name} has to be a contiguous {dtype} tensor {shape} on q's GPU")
+    d = abi.ZiAttentionDesc(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), *strides, B, H, Hk, n, m,
+                            128 ** -0.5 if scale is None else scale, softcap, _ptr(slopes), 1 if causal else 0,
+                            _ptr(prefix_len), _ptr(kv_len), _ptr(q_doc), _ptr(k_doc))
+    _launch(device, "zi_attention_masked", ctypes.byref(d))
     return out
 
 
