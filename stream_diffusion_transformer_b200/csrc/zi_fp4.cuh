@@ -11,6 +11,7 @@
 #pragma once
 #include <cuda_fp4.h>
 
+#include "zi_attention.cuh"  // packed fp32 pairs
 #include "zi_common.cuh"
 #include "zi_gemm.cuh"
 
@@ -40,45 +41,64 @@ ZI_DEV size_t scale_word(int row, int tile, int tiles_x) {
 
 constexpr int kRowsThreads = 256;
 
-// 16 consecutive elements of a row as fp32, and the largest |x| as its bit pattern (an
-// integer maximum, so that infinities and NaN come out on top instead of being dropped).
-struct Span16 {
-  float v[16];
-  uint32_t amax;
+// 16 consecutive elements of a row, as loaded.
+template <typename TIn>
+struct Span {
+  uint4 w[sizeof(TIn)];  // 2 or 4 of 16 bytes
 };
 
-ZI_DEV Span16 load_span(const float* p) {
-  Span16 s;
-  s.amax = 0;
+template <typename TIn>
+ZI_DEV Span<TIn> load_span(const TIn* p) {
+  Span<TIn> s;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(p) + q);
-    const uint32_t b[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      s.v[4 * q + i] = __uint_as_float(b[i]);
-      s.amax = max(s.amax, b[i] & 0x7FFFFFFFu);
-    }
-  }
+  for (int i = 0; i < int(sizeof(TIn)); ++i) s.w[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
   return s;
 }
 
-ZI_DEV Span16 load_span(const uint16_t* p) {
-  Span16 s;
-  s.amax = 0;
+// The largest |x| as its bit pattern (an integer maximum, so that infinities and NaN come out
+// on top instead of being dropped).
+ZI_DEV uint32_t span_amax(const Span<float>& s) {
+  uint32_t m = 0;
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(p) + q);
-    const uint32_t b[4] = {w.x, w.y, w.z, w.w};
+  for (int i = 0; i < 4; ++i)
+    m = max(m, max(max(s.w[i].x & 0x7FFFFFFFu, s.w[i].y & 0x7FFFFFFFu), max(s.w[i].z & 0x7FFFFFFFu, s.w[i].w & 0x7FFFFFFFu)));
+  return m;
+}
+ZI_DEV uint32_t span_amax(const Span<uint16_t>& s) {
+  uint32_t m = 0;  // two 16-bit maxima
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t lo = b[i] << 16, hi = b[i] & 0xFFFF0000u;
-      s.v[8 * q + 2 * i] = __uint_as_float(lo);
-      s.v[8 * q + 2 * i + 1] = __uint_as_float(hi);
-      s.amax = max(s.amax, max(lo & 0x7FFFFFFFu, hi & 0x7FFFFFFFu));
+  for (int i = 0; i < 2; ++i) {
+    m = __vmaxu2(m, __vmaxu2(s.w[i].x & 0x7FFF7FFFu, s.w[i].y & 0x7FFF7FFFu));
+    m = __vmaxu2(m, __vmaxu2(s.w[i].z & 0x7FFF7FFFu, s.w[i].w & 0x7FFF7FFFu));
+  }
+  return max(m << 16, m & 0xFFFF0000u);
+}
+
+ZI_DEV void span_values(const Span<float>& s, float* v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[4 * i] = __uint_as_float(s.w[i].x);
+    v[4 * i + 1] = __uint_as_float(s.w[i].y);
+    v[4 * i + 2] = __uint_as_float(s.w[i].z);
+    v[4 * i + 3] = __uint_as_float(s.w[i].w);
+  }
+}
+ZI_DEV void span_values(const Span<uint16_t>& s, float* v) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t b[4] = {s.w[i].x, s.w[i].y, s.w[i].z, s.w[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[8 * i + 2 * k] = __uint_as_float(b[k] << 16);
+      v[8 * i + 2 * k + 1] = __uint_as_float(b[k] & 0xFFFF0000u);
     }
   }
-  return s;
+}
+
+ZI_DEV float rcp_approx(float x) {  // within 2^-22 or so
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 constexpr uint32_t kInfBits = 0x7F800000u;
@@ -121,7 +141,8 @@ ZI_DEV float off_border(float q, float a, float b) {
 ZI_DEV uint32_t nv_scale(uint32_t amax, uint32_t row_exp) {
   if (amax >= kInfBits) return 0x7Fu;
   const float t = __uint_as_float(amax) * exp_float(254u - row_exp);  // amax / r, exact
-  const float q = off_border(__fdiv_rn(t, 6.f), t, 6.f);
+  const float q0 = t * (1.f / 6.f);
+  const float q = off_border(fmaf(fmaf(-q0, 6.f, t), 1.f / 6.f, q0), t, 6.f);  // one Newton step on the residual
   return __nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
 }
 
@@ -130,8 +151,7 @@ ZI_DEV float e4m3_float(uint32_t byte) {
   return __half2float(__half(h));
 }
 
-// 16 e2m1 codes (8 bytes, in column order) of v[i] = x[i] / scale, to nearest even,
-// saturating at 6.
+// 16 e2m1 codes (8 bytes, in column order) of v, to nearest even, saturating at 6.
 ZI_DEV uint2 codes16(const float* v) {
   uint32_t w[2];
 #pragma unroll
@@ -147,10 +167,61 @@ ZI_DEV uint2 codes16(const float* v) {
   return make_uint2(w[0], w[1]);
 }
 
-// Rows of x [rows, cols] to codes, block scales and (NVFP4) row scales.  One thread per 16
-// columns, `tpr` threads (a power of two, up to the whole CTA) per row, NB spans per thread
-// for rows wider than 16 tpr.  x is read once; an NVFP4 row waits in registers for its
-// maximum.  Rows past the end up to the scale tile's 128 only write their zero scales.
+// v[i] to v[i] / (sc r), an NVFP4 block's elements in units of its scales, such that e2m1's rounding of it
+// decides as on the exact quotient.  x times a reciprocal is off by 2^-23 or so, enough to miss a tie; adding and
+// taking off 48 rounds it to a multiple of 2^-18 in the same FMA (quotients are below 9.1, and within 2^-19 of the
+// exact ones before).  The ties 0.25, 0.75, ... 5 are such multiples, so a quotient lands on one only from near it:
+// - a bf16 x (8 bits) over a scale of 4 bits is a tie exactly or at least 2^-8 of its value away from it;
+// - an fp32 x can be that near: a span with a quotient on a multiple of 1/4 (one span in 4000) is done again by a
+//   division whose remainder says on which side of the tie it lies.
+template <bool EXACT24>
+ZI_DEV void nv_units(float* v, float sc, uint32_t row_exp) {
+  float inv = rcp_approx(sc);
+  if (row_exp < 28u) {  // 1 / r would take the factor out of range: tiny rows, scaled first
+    const float rinv = exp_float(254u - row_exp);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] *= rinv;
+    row_exp = 127u;
+  } else {
+    inv *= exp_float(254u - row_exp);
+  }
+  constexpr float kSnap = 48.f;
+  const uint64_t inv2 = f2_pack(inv, inv), up = f2_pack(kSnap, kSnap), down = f2_pack(-kSnap, -kSnap);
+  float w[16];
+  uint32_t low = ~0u;
+#pragma unroll
+  for (int e = 0; e < 16; e += 2) {
+    const uint64_t at = f2_fma(f2_pack(v[e], v[e + 1]), inv2, up);
+    if (EXACT24) low = min(low, min(uint32_t(at) << 16, uint32_t(at >> 32) << 16));
+    f2_unpack(f2_add(at, down), w[e], w[e + 1]);
+  }
+  if (EXACT24 && low == 0u) {
+    const float rinv = exp_float(254u - row_exp), i1 = rcp_approx(sc);
+#pragma unroll 1
+    for (int h = 0; h < 4; ++h) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        // 4 h + e without indexing the registers: the loop rotates them
+        const float xr = v[e] * rinv, v0 = xr * i1;
+        const float v1 = fmaf(fmaf(-v0, sc, xr), i1, v0);  // one Newton step on the residual
+        const float r = copysignf(off_border(v1, xr, sc), xr);
+        v[e] = v[e + 4];
+        v[e + 4] = v[e + 8];
+        v[e + 8] = v[e + 12];
+        v[e + 12] = r;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = copysignf(w[e], v[e]);  // the sign of a zero is kept
+  }
+}
+
+// Rows of x [rows, cols] to codes, block scales and (NVFP4) row scales.  `tpr` threads (a
+// power of two, up to the whole CTA) per row, NB spans of 16 columns per thread, span i on
+// thread i % tpr.  x is read once, all of a thread's spans at once, and an NVFP4 row waits
+// in registers, as it was loaded, for its maximum.  Rows past the end up to the scale tile's
+// 128 only write their zero scales.
 template <int FMT, typename TIn, int NB>
 __global__ void __launch_bounds__(kRowsThreads) quantize_kernel(const TIn* __restrict__ x, int rows, int cols, int tpr,
                                                                uint8_t* __restrict__ q, uint8_t* __restrict__ bs,
@@ -162,19 +233,25 @@ __global__ void __launch_bounds__(kRowsThreads) quantize_kernel(const TIn* __res
   const int tiles_x = tiles_along<FMT>(cols);
   const int rows_pad = tiles_down(rows) * 128;
 
-  Span16 s[NB];
-  uint32_t am = 0;
+  Span<TIn> s[NB];
 #pragma unroll
   for (int k = 0; k < NB; ++k) {
     const int i = sub + k * tpr;
-    s[k].amax = 0;
     if (row < rows && i < spans) {
       s[k] = load_span(x + size_t(row) * cols + size_t(i) * 16);
-      if (FMT == NV && s[k].amax < kInfBits) am = max(am, s[k].amax);
+    } else {
+#pragma unroll
+      for (int e = 0; e < int(sizeof(TIn)); ++e) s[k].w[e] = make_uint4(0, 0, 0, 0);
     }
   }
   uint32_t row_exp = 127u;
   if constexpr (FMT == NV) {
+    uint32_t am = 0;
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      const uint32_t a = span_amax(s[k]);
+      if (a < kInfBits) am = max(am, a);
+    }
     for (int o = (tpr < 32 ? tpr : 32) >> 1; o > 0; o >>= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
     if (tpr > 32) {  // the row spans warps
       if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = am;
@@ -189,42 +266,31 @@ __global__ void __launch_bounds__(kRowsThreads) quantize_kernel(const TIn* __res
   for (int k = 0; k < NB; ++k) {
     const int i = sub + k * tpr;
     const bool have = row < rows && i < spans;
+    uint32_t amax = span_amax(s[k]);
+    if (FMT == MX) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     uint32_t byte = 0;
-    if constexpr (FMT == MX) {
-      const uint32_t both = max(s[k].amax, __shfl_xor_sync(0xffffffffu, s[k].amax, 1));
-      if (have) {
-        byte = mx_scale(both);
-        if (both < kInfBits) {
-          const float inv = exp_float(254u - byte);
+    if (have) {
+      float v[16];
+      span_values(s[k], v);
+      if constexpr (FMT == MX) {
+        byte = mx_scale(amax);
+        const uint64_t inv2 = f2_pack(exp_float(254u - byte), exp_float(254u - byte));
 #pragma unroll
-          for (int e = 0; e < 16; ++e) s[k].v[e] *= inv;  // exact (a power of two), or far below half a step
-        }
-      }
-      if (both >= kInfBits) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) s[k].v[e] = 0.f;
-      }
-    } else {
-      if (have) {
-        byte = nv_scale(s[k].amax, row_exp);
-        const float sc = e4m3_float(byte);
-        if (byte == 0u || byte == 0x7Fu) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) s[k].v[e] = byte ? 0.f : copysignf(0.f, s[k].v[e]);
+        for (int e = 0; e < 16; e += 2)  // exact (a power of two), or far below half a step
+          f2_unpack(f2_mul(f2_pack(v[e], v[e + 1]), inv2), v[e], v[e + 1]);
+      } else {
+        byte = nv_scale(amax, row_exp);
+        if (byte != 0u && byte != 0x7Fu) {
+          nv_units<sizeof(TIn) == 4>(v, e4m3_float(byte), row_exp);
         } else {
-          const float rinv = exp_float(254u - row_exp), inv = __frcp_rn(sc);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float xr = s[k].v[e] * rinv;  // exact, or far below half a step
-            const float v0 = xr * inv;
-            const float v1 = fmaf(fmaf(-v0, sc, xr), inv, v0);  // one Newton step on the residual
-            // a bf16 x has 8 bits: its quotient hits a border exactly or lies far from it.  The sign of a zero is kept.
-            s[k].v[e] = copysignf(sizeof(TIn) == 4 ? off_border(v1, xr, sc) : v1, xr);
-          }
+          for (int e = 0; e < 16; ++e) v[e] = copysignf(0.f, v[e]);
         }
       }
+      uint2 c = codes16(v);
+      if (amax >= kInfBits) c = make_uint2(0, 0);
+      *reinterpret_cast<uint2*>(q + size_t(row) * (cols / 2) + size_t(i) * 8) = c;
     }
-    if (have) *reinterpret_cast<uint2*>(q + size_t(row) * (cols / 2) + size_t(i) * 8) = codes16(s[k].v);
     // four block scales to a word
     constexpr int kStep = kBlock<FMT> / 16;  // threads per block
     uint32_t word = byte;
@@ -236,49 +302,49 @@ __global__ void __launch_bounds__(kRowsThreads) quantize_kernel(const TIn* __res
   }
 }
 
-// The values that codes and scales stand for, bf16 or fp32: one thread per 16 columns.
+// The values that codes and scales stand for, bf16 or fp32.  `tpr` threads per row, 8 columns
+// (one 16- or 32-byte store) per thread at a time, so that a warp's stores are contiguous.
 template <int FMT, typename TOut>
 __global__ void __launch_bounds__(kRowsThreads) dequantize_kernel(const uint8_t* __restrict__ q,
                                                                  const uint8_t* __restrict__ bs,
                                                                  const float* __restrict__ rs, int rows, int cols,
-                                                                 TOut* __restrict__ y) {
-  const int spans = cols / 16;
-  const size_t t = size_t(blockIdx.x) * kRowsThreads + threadIdx.x;
-  if (t >= size_t(rows) * spans) return;
-  const int row = int(t / spans), i = int(t % spans);
-  const int block = i * 16 / kBlock<FMT>;
-  const uint32_t byte = bs[scale_word(row, block >> 2, tiles_along<FMT>(cols)) + (block & 3)];
-  float lo = 1.f, hi;  // value = code * lo * hi, the last product the only one that may round (below the normal numbers)
-  if constexpr (FMT == MX) {
-    // 2^(c - 127) in two factors: c = 0 lies below the normal numbers, c = 255 is NaN
-    hi = byte == 0xFFu ? __uint_as_float(0x7FC00000u) : exp_float(byte == 0 ? 1u : byte);
-    lo = byte == 0 ? 0.5f : 1.f;
-  } else {
-    lo = e4m3_float(byte);
-    hi = rs[row];
-  }
-  const uint2 w = *reinterpret_cast<const uint2*>(q + t * 8);
-  const uint32_t ww[2] = {w.x, w.y};
-  float v[16];
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
+                                                                 int tpr, TOut* __restrict__ y) {
+  const int sub = threadIdx.x & (tpr - 1);
+  const int row = int(blockIdx.x * (kRowsThreads / tpr) + threadIdx.x / tpr);
+  if (row >= rows) return;
+  const int eights = cols / 8, tiles_x = tiles_along<FMT>(cols);
+  const float r = FMT == NV ? __ldg(rs + row) : 1.f;
+  const uint8_t* scales = bs + scale_word(row, 0, tiles_x);
+  const uint32_t* codes = reinterpret_cast<const uint32_t*>(q + size_t(row) * (cols / 2));
+  TOut* out = y + size_t(row) * cols;
+#pragma unroll 4
+  for (int i = sub; i < eights; i += tpr) {
+    const int block = i * 8 / kBlock<FMT>;
+    const uint32_t byte = __ldg(scales + (block >> 2) * kTileBytes + (block & 3));
+    const uint32_t w = __ldg(codes + i);
+    float sc;
+    if constexpr (FMT == MX) {
+      // 2^(c - 127): c = 0 lies below the normal numbers, c = 255 is NaN
+      sc = byte == 0xFFu ? __uint_as_float(0x7FC00000u) : byte == 0 ? __uint_as_float(0x00400000u) : exp_float(byte);
+    } else {
+      sc = e4m3_float(byte) * r;
+    }
+    const uint64_t sc2 = f2_pack(sc, sc);
+    float v[8];
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-      const __half2_raw r = __nv_cvt_fp4x2_to_halfraw2(__nv_fp4x2_storage_t((ww[h] >> (8 * b)) & 0xFFu), __NV_E2M1);
-      const float2 f = __half22float2(__half2(r));
-      v[8 * h + 2 * b] = f.x * lo * hi;
-      v[8 * h + 2 * b + 1] = f.y * lo * hi;
+      const __half2_raw c = __nv_cvt_fp4x2_to_halfraw2(__nv_fp4x2_storage_t((w >> (8 * b)) & 0xFFu), __NV_E2M1);
+      const float2 f = __half22float2(__half2(c));
+      f2_unpack(f2_mul(f2_pack(f.x, f.y), sc2), v[2 * b], v[2 * b + 1]);
     }
-  if constexpr (sizeof(TOut) == 4) {
-    float4* d = reinterpret_cast<float4*>(y + t * 16);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) d[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-  } else {
-    uint4* d = reinterpret_cast<uint4*>(y + t * 16);
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-      d[k] = make_uint4(pack_bf16x2(v[8 * k], v[8 * k + 1]), pack_bf16x2(v[8 * k + 2], v[8 * k + 3]),
-                        pack_bf16x2(v[8 * k + 4], v[8 * k + 5]), pack_bf16x2(v[8 * k + 6], v[8 * k + 7]));
+    if constexpr (sizeof(TOut) == 4) {
+      float4* d = reinterpret_cast<float4*>(out + size_t(i) * 8);
+      d[0] = make_float4(v[0], v[1], v[2], v[3]);
+      d[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+      *reinterpret_cast<uint4*>(out + size_t(i) * 8) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                                  pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    }
   }
 }
 
