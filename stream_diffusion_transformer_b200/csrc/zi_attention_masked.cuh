@@ -55,26 +55,31 @@ ZI_DEV float tanh_exp(float x) {
 // ------------------------------------------------------------------ few queries
 // One CTA per 16 rows of a key head (a row is one query of one head of the group, row =
 // query * group + head in the group) and share of the keys; a cluster of CTAs shares a
-// tile's keys.  Bound by reading K and V: each of the 4 warps streams its own chunks of 32
-// keys through a private smem ring with cp.async (3 chunks of K and V deep, 48 KB per
-// warp), takes scores and products with mma.sync m16n8k16 (16 rows padded: the tensor work
-// is small beside the loads) and keeps its own running maximum and sum.  The warps' and
+// tile's keys.  Bound by reading K and V: each of the 4 warps streams its own chunks of 16
+// keys through a private smem ring with TMA (3 chunks of K and V deep, 24 KB per warp, two
+// CTAs per SM), takes scores and products with mma.sync m16n8k16 (16 rows padded: the tensor
+// work is small beside the loads) and keeps its own running maximum and sum.  The warps' and
 // then the cluster's partials are joined in a fixed order.
 namespace few {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kChunk = 32;                       // keys per chunk
+constexpr int kChunk = 16;                       // keys per chunk
 constexpr int kRing = 3;
-constexpr uint32_t kHalfBytes = kChunk * 256;    // K or V of a chunk: 32 rows of 256 bytes
-constexpr uint32_t kChunkBytes = 2 * kHalfBytes;
+constexpr uint32_t kBox = kChunk * 128;          // 16 rows of 64 dims, 128-byte swizzle
+constexpr uint32_t kChunkBytes = 4 * kBox;       // K dims 0..63, 64..127, then V
 constexpr uint32_t kWarpBytes = kRing * kChunkBytes;
-constexpr uint32_t kSmemBytes = kWarps * kWarpBytes;
+constexpr uint32_t kBar = kWarps * kWarpBytes;
+constexpr uint32_t kSmemBytes = kBar + 256 + 1024;
 constexpr uint32_t kPartFloats = 16 * 128 + 32;  // O [16][128], then m [16], l [16]
-static_assert(kWarps * kPartFloats * 4 + kPartFloats * 4 <= kSmemBytes, "partials reuse the ring");
+static_assert((kWarps + 1) * kPartFloats * 4 <= kBar, "partials reuse the ring");
 }  // namespace few
 
-ZI_DEV void cp_async16(uint32_t dst, const void* src, bool have) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(have ? 16 : 0) : "memory");
+ZI_DEV void tma_load_4d(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::
+          "r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
 }
 
 ZI_DEV void ldsm4(uint32_t* r, uint32_t addr) {
@@ -96,25 +101,72 @@ ZI_DEV void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__global__ void __launch_bounds__(few::kThreads) attention_few_kernel(MaskedParams p, int splits) {
+ZI_DEV float ld_cluster_f32(uint32_t addr, int rank) {
+  float x;
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(a) : "memory");
+  return x;
+}
+ZI_DEV float4 ld_cluster_f4(uint32_t addr, int rank) {
+  float4 x;
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+               : "r"(a)
+               : "memory");
+  return x;
+}
+
+__global__ void __launch_bounds__(few::kThreads)
+    attention_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, MaskedParams p,
+                         int splits) {
   using namespace few;
-  extern __shared__ __align__(128) uint8_t ring[];
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kBar);  // [kWarps][kRing]
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + kWarps * kRing);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = int(blockIdx.x) % splits, tile = int(blockIdx.x) / splits;
   const int hk = blockIdx.y, b = blockIdx.z;
   const int rows = p.q_len * p.group;
   const int row0 = tile * 16;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kWarps * kRing; ++i) mbar_init(bars + i, 1);
+    *abort_flag = device_error_set() ? 1 : 0;  // an earlier kernel timed out: leave everything untouched
+    fence_mbar_init();
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
+  }
+  __syncthreads();
+
   const int n = masked_keys(p, b);
   // keys that any row of the tile may see: limits grow with the query
   const int i_last = (min(row0 + 16, rows) - 1) / p.group;
-  const int end = masked_limit(p, b, i_last, n);
+  const int end = *abort_flag ? 0 : masked_limit(p, b, i_last, n);
   const int chunks = (end + kChunk - 1) / kChunk;
-  const int c0 = int(static_cast<long long>(rank) * chunks / splits);
+  const int c0 = int(static_cast<long long>(rank) * chunks / splits) + warp;
   const int c1 = int(static_cast<long long>(rank + 1) * chunks / splits);
+  uint8_t* ring = smem + warp * kWarpBytes;
+  uint64_t* full = bars + warp * kRing;
+  auto load = [&](int c, int slot) {  // lane 0
+    uint8_t* dst = ring + slot * kChunkBytes;
+    mbar_arrive_expect_tx(&full[slot], kChunkBytes);
+    tma_load_4d(dst, &tmK, &full[slot], 0, hk, c * kChunk, b);
+    tma_load_4d(dst + kBox, &tmK, &full[slot], 64, hk, c * kChunk, b);
+    tma_load_4d(dst + 2 * kBox, &tmV, &full[slot], 0, hk, c * kChunk, b);
+    tma_load_4d(dst + 3 * kBox, &tmV, &full[slot], 64, hk, c * kChunk, b);
+  };
+  if (lane == 0)
+    for (int s = 0; s < kRing; ++s)
+      if (c0 + s * kWarps < c1) load(c0 + s * kWarps, s);
 
-  // this lane's two rows (fragment rows lane / 4 and lane / 4 + 8)
+  // this lane's two rows (fragment rows lane / 4 and lane / 4 + 8) and their Q fragments: 8 steps of 16 dims
   int lim[2], pos[2], doc[2];
   float slope[2];
+  uint32_t qf[8][4];
   const int gid = lane >> 2, tid = lane & 3;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -126,70 +178,48 @@ __global__ void __launch_bounds__(few::kThreads) attention_few_kernel(MaskedPara
     doc[h] = have && p.q_doc ? __ldg(p.q_doc + size_t(b) * p.q_len + i) : 0;
     if (doc[h] < 0) lim[h] = 0;
     slope[h] = have && p.slopes ? __ldg(p.slopes + hk * p.group + g) * 1.4426950408889634f : 0.f;
-  }
-  // Q fragments: 8 steps of 16 dims
-  uint32_t qf[8][4];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int r = row0 + gid + 8 * h;
-    const int i = r / p.group, g = r - i * p.group;
     const uint16_t* src = p.q + b * p.q_bs + i * p.q_rs + (hk * p.group + g) * p.q_hs;
 #pragma unroll
     for (int s = 0; s < 8; ++s) {
-      qf[s][h] = r < rows ? *reinterpret_cast<const uint32_t*>(src + s * 16 + tid * 2) : 0u;
-      qf[s][2 + h] = r < rows ? *reinterpret_cast<const uint32_t*>(src + s * 16 + 8 + tid * 2) : 0u;
+      qf[s][h] = have ? __ldg(reinterpret_cast<const uint32_t*>(src + s * 16 + tid * 2)) : 0u;
+      qf[s][2 + h] = have ? __ldg(reinterpret_cast<const uint32_t*>(src + s * 16 + 8 + tid * 2)) : 0u;
     }
   }
-  const uint16_t* kb = p.k + b * p.k_bs + hk * p.k_hs;
-  const uint16_t* vb = p.v + b * p.v_bs + hk * p.v_hs;
+  const int all_lim = __reduce_min_sync(0xffffffffu, min(row0 + gid < rows ? lim[0] : 0x7fffffff,
+                                                         row0 + gid + 8 < rows ? lim[1] : 0x7fffffff));
   const int* kd = p.k_doc ? p.k_doc + size_t(b) * p.kv_len : nullptr;
-  const uint32_t base = smem_u32(ring) + warp * kWarpBytes;
-
-  // Chunk c of this warp: rows of 16 16-byte pieces, piece x of row r at slot x ^ (r & 7).  Keys past the
-  // element's end are filled with zeros, so whatever stands there never meets a product.
-  auto load = [&](int c, int slot) {
-    const int key0 = c * kChunk;
-    const int half = lane >> 4, x = lane & 15;
-#pragma unroll
-    for (int r = 0; r < kChunk; r += 2) {
-      const int row = r + half, key = key0 + row;
-      const bool have = key < n && (!kd || __ldg(kd + key) >= 0);
-      const size_t kk = have ? key : 0;
-      const uint32_t dst = base + slot * kChunkBytes + row * 256 + ((x ^ (row & 7)) << 4);
-      cp_async16(dst, kb + kk * p.k_rs + x * 8, have);
-      cp_async16(dst + kHalfBytes, vb + kk * p.v_rs + x * 8, have);
-    }
-  };
 
   float o[16][4];
 #pragma unroll
   for (int t = 0; t < 16; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-
-  int c = c0 + warp;
+  const int lr = lane & 7, lm = lane >> 3;  // ldmatrix: this lane's row in matrix lm
+  int slot = 0;
+  uint32_t phase = 0;
+  for (int c = c0; c < c1; c += kWarps) {
+    // ids of the keys 2 tid, 2 tid + 1 and 8 further, as the fragments hold them
+    int id[4] = {0, 0, 0, 0};
+    const bool part = kd || (c + 1) * kChunk > all_lim;
+    uint32_t used[2] = {~0u, ~0u};  // V rows that some query may see, as pairs of bf16
+    if (part) {
 #pragma unroll
-  for (int s = 0; s < kRing - 1; ++s) {
-    if (c + s * kWarps < c1) load(c + s * kWarps, s);
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  }
-  for (int slot = 0; c < c1; c += kWarps) {
-    const int ahead = c + (kRing - 1) * kWarps;
-    if (ahead < c1) load(ahead, slot == 0 ? kRing - 1 : slot - 1);
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
-    __syncwarp();
-    const uint32_t ks = base + slot * kChunkBytes, vs = ks + kHalfBytes;
-    slot = slot + 1 == kRing ? 0 : slot + 1;
-    float s[4][4];
+      for (int e = 0; e < 4; ++e) {
+        const int key = c * kChunk + (e >> 1) * 8 + tid * 2 + (e & 1);
+        if (kd) id[e] = key < n ? __ldg(kd + key) : -1;
+        if (key >= n || id[e] < 0) used[e >> 1] &= (e & 1) ? 0x0000FFFFu : 0xFFFF0000u;
+      }
+    }
+    if (!mbar_wait(&full[slot], phase, abort_flag, ZI_DEVERR_TIMEOUT_SOFTMAX)) break;
+    const uint32_t ks = smem_u32(ring + slot * kChunkBytes), vs = ks + 2 * kBox;
+    float s[2][4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
-    const int lr = lane & 7, lm = lane >> 3;  // ldmatrix: this lane's row in matrix lm
+    for (int t = 0; t < 2; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
 #pragma unroll
     for (int kp = 0; kp < 4; ++kp) {  // two 16-dim steps at a time
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
+      for (int t = 0; t < 2; ++t) {
         uint32_t kf[4];
-        ldsm4(kf, ks + (t * 8 + lr) * 256 + (((kp * 4 + lm) ^ lr) << 4));
+        ldsm4(kf, ks + (kp >> 1) * kBox + (t * 8 + lr) * 128 + ((((kp & 1) * 4 + lm) ^ lr) << 4));
         mma16816(s[t], qf[2 * kp], kf[0], kf[1]);
         mma16816(s[t], qf[2 * kp + 1], kf[2], kf[3]);
       }
@@ -197,66 +227,90 @@ __global__ void __launch_bounds__(few::kThreads) attention_few_kernel(MaskedPara
     // scores to the exp2 domain, masked
     float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
+    for (int t = 0; t < 2; ++t) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int h = e >> 1, key = c * kChunk + t * 8 + tid * 2 + (e & 1);
         float y = s[t][e] * p.scale_log2;
         if (p.cap_log2 != 0.f) y = tanh_exp(y) * p.cap_log2;
         if (p.slopes) y -= slope[h] * fabsf(float(pos[h] - key));
-        bool see = key < lim[h];
-        if (kd) see = see && __ldg(kd + (key < n ? key : 0)) == doc[h];
-        s[t][e] = see ? y : -INFINITY;
-        mx[h] = fmaxf(mx[h], s[t][e]);
+        if (part && (key >= lim[h] || (kd && id[t * 2 + (e & 1)] != doc[h]))) y = -INFINITY;
+        s[t][e] = y;
+        mx[h] = fmaxf(mx[h], y);
       }
     }
-    float alpha[2], mu[2];
+    float mu[2];
+    bool grows = false;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
       mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
-      const float mn = fmaxf(m[h], mx[h]);
-      mu[h] = mn == -INFINITY ? 0.f : mn;  // a row that has seen nothing yet
-      alpha[h] = fast_exp2(m[h] - mu[h]);
-      m[h] = mn;
-      l[h] *= alpha[h];
+      grows = grows || mx[h] > m[h] + 8.f;  // the maximum may lag by 2^8
     }
-    uint32_t pf[2][4];
+    if (__any_sync(0xffffffffu, grows)) {
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
+      for (int h = 0; h < 2; ++h) {
+        if (mx[h] > m[h] + 8.f) {  // each row by its own scores alone
+          const float alpha = m[h] == -INFINITY ? 0.f : fast_exp2(m[h] - mx[h]);
+          m[h] = mx[h];
+          l[h] *= alpha;
+#pragma unroll
+          for (int t = 0; t < 16; ++t) {
+            o[t][2 * h] *= alpha;
+            o[t][2 * h + 1] *= alpha;
+          }
+        }
+      }
+    }
+    mu[0] = m[0] == -INFINITY ? 0.f : m[0];  // a row that has seen nothing yet
+    mu[1] = m[1] == -INFINITY ? 0.f : m[1];
+    uint32_t pf[4];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
       const float e0 = fast_exp2(s[t][0] - mu[0]), e1 = fast_exp2(s[t][1] - mu[0]);
       const float e2 = fast_exp2(s[t][2] - mu[1]), e3 = fast_exp2(s[t][3] - mu[1]);
       l[0] += e0 + e1;
       l[1] += e2 + e3;
       // probabilities in bf16 for the tensor core: half a step of 2^-8 each, averaged over the keys
-      pf[t >> 1][(t & 1) * 2] = pack_bf16x2(e0, e1);
-      pf[t >> 1][(t & 1) * 2 + 1] = pack_bf16x2(e2, e3);
+      pf[t * 2] = pack_bf16x2(e0, e1);
+      pf[t * 2 + 1] = pack_bf16x2(e2, e3);
     }
 #pragma unroll
-    for (int t = 0; t < 16; ++t) {
-      o[t][0] *= alpha[0];
-      o[t][1] *= alpha[0];
-      o[t][2] *= alpha[1];
-      o[t][3] *= alpha[1];
+    for (int t = 0; t < 16; t += 2) {
+      uint32_t vf[4];  // keys 0..15 x dims 8 t .. 8 t + 15
+      const int row = (lm & 1) * 8 + lr, x = t + (lm >> 1);
+      ldsm4_t(vf, vs + (x >> 3) * kBox + row * 128 + (((x & 7) ^ lr) << 4));
+      if (part) {  // zero probabilities times what stands in unused rows could be NaN
+        vf[0] &= used[0];
+        vf[1] &= used[1];
+        vf[2] &= used[0];
+        vf[3] &= used[1];
+      }
+      mma16816(o[t], pf, vf[0], vf[1]);
+      mma16816(o[t + 1], pf, vf[2], vf[3]);
     }
-#pragma unroll
-    for (int t = 0; t < 16; ++t) {
-      uint32_t vf[4];  // keys 0..31 x dims 8 t .. 8 t + 7
-      const int row = lm * 8 + lr;
-      ldsm4_t(vf, vs + row * 256 + ((t ^ (row & 7)) << 4));
-      mma16816(o[t], pf[0], vf[0], vf[1]);
-      mma16816(o[t], pf[1], vf[2], vf[3]);
+    __syncwarp();  // every lane is done with the slot
+    if (lane == 0 && c + kRing * kWarps < c1) load(c + kRing * kWarps, slot);
+    if (++slot == kRing) {
+      slot = 0;
+      phase ^= 1u;
     }
-    __syncwarp();  // every lane is done with the slot before it is refilled
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");
+  if (*abort_flag) {  // a wait ran out: let the copies already issued land before the ring is left
+    volatile int never = 0;
+    for (int s = 0; s < kRing; ++s)
+      if (c0 + s * kWarps < c1) mbar_wait(&full[s], 0, &never, ZI_DEVERR_TIMEOUT_DRAIN, 1000000ull);
+    const unsigned long long t0 = globaltimer();
+    while (globaltimer() - t0 < 200000ull) {
+    }
+  }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
     l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
   }
   __syncthreads();  // the rings become the warps' partials
-  float* parts = reinterpret_cast<float*>(ring);
+  float* parts = reinterpret_cast<float*>(smem);
   float* mine = parts + warp * kPartFloats;
 #pragma unroll
   for (int t = 0; t < 16; ++t)
@@ -274,7 +328,8 @@ __global__ void __launch_bounds__(few::kThreads) attention_few_kernel(MaskedPara
   // join the warps: thread d holds column d of every row
   float* cta = parts + kWarps * kPartFloats;
   const int d = threadIdx.x;
-  for (int r = 0; r < 16; ++r) {
+  const int live = min(16, rows - row0);
+  for (int r = 0; r < live; ++r) {
     float mm = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, parts[w * kPartFloats + 2048 + r]);
@@ -293,35 +348,30 @@ __global__ void __launch_bounds__(few::kThreads) attention_few_kernel(MaskedPara
     }
   }
   if (splits > 1) cluster_sync(); else __syncthreads();
-  // join the cluster: this CTA's share of the 16 rows, ranks in order
-  const int r0 = rank * 16 / splits, r1 = (rank + 1) * 16 / splits;
+  // join the cluster: this CTA's share of the rows, ranks in order
+  bool bad = false;
+  for (int w = 0; w < splits; ++w)
+    bad = bad || (splits > 1 ? __float_as_int(ld_cluster_f32(smem_u32(const_cast<int*>(abort_flag)), w)) : *abort_flag) != 0;
   const uint32_t cta_addr = smem_u32(cta);
-  auto peer = [&](int r, int idx) {
-    float x;
-    uint32_t addr = cta_addr + uint32_t(idx) * 4;
-    if (splits > 1) {
-      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(addr), "r"(r));
-      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
-    } else {
-      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
+  for (int r = rank; r < live && !bad; r += splits) {
+    float mm = -INFINITY, mw[8];
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      mw[w] = w >= splits ? -INFINITY : splits > 1 ? ld_cluster_f32(cta_addr + (2048 + r) * 4, w) : cta[2048 + r];
+      mm = fmaxf(mm, mw[w]);
     }
-    return x;
-  };
-  for (int r = r0; r < r1; ++r) {
-    const int row = row0 + r;
-    if (row >= rows) break;
-    float mm = -INFINITY;
-    for (int w = 0; w < splits; ++w) mm = fmaxf(mm, peer(w, 2048 + r));
     const float mu = mm == -INFINITY ? 0.f : mm;
     float acc = 0.f, ll = 0.f;
-    for (int w = 0; w < splits; ++w) {
-      const float f = fast_exp2(peer(w, 2048 + r) - mu);
-      acc = fmaf(f, peer(w, r * 128 + d), acc);
-      ll = fmaf(f, peer(w, 2064 + r), ll);
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      if (w < splits) {
+        const float f = fast_exp2(mw[w] - mu);
+        acc = fmaf(f, splits > 1 ? ld_cluster_f32(cta_addr + (r * 128 + d) * 4, w) : cta[r * 128 + d], acc);
+        ll = fmaf(f, splits > 1 ? ld_cluster_f32(cta_addr + (2064 + r) * 4, w) : cta[2064 + r], ll);
+      }
     }
-    const int i = row / p.group, g = row - i * p.group;
-    const float y = ll > 0.f ? acc / ll : 0.f;
-    const __nv_bfloat16 yb = __float2bfloat16_rn(y);
+    const int row = row0 + r, i = row / p.group, g = row - i * p.group;
+    const __nv_bfloat16 yb = __float2bfloat16_rn(ll > 0.f ? acc / ll : 0.f);  // a row that sees no key: 0
     p.out[b * p.o_bs + i * p.o_rs + (hk * p.group + g) * p.o_hs + d] = *reinterpret_cast<const uint16_t*>(&yb);
   }
   if (splits > 1) cluster_sync();  // no CTA leaves while its partial may be read
@@ -368,32 +418,6 @@ ZI_DEV uint64_t cap_poly_pair(uint64_t s2, const float* c) {
   r = f2_fma(r, u, f2_pack(c[1], c[1]));
   r = f2_fma(r, u, f2_pack(c[0], c[0]));
   return f2_mul(r, s2);
-}
-
-ZI_DEV void tma_load_4d(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z, int w) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::
-          "r"(smem_u32(smem_dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
-      : "memory");
-}
-
-ZI_DEV float ld_cluster_f32(uint32_t addr, int rank) {
-  float x;
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(a) : "memory");
-  return x;
-}
-ZI_DEV float4 ld_cluster_f4(uint32_t addr, int rank) {
-  float4 x;
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
-               : "r"(a)
-               : "memory");
-  return x;
 }
 
 // The low word of a 128-byte-swizzled operand descriptor (smem_desc_sw128); its high word is

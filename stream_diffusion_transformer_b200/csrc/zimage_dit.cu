@@ -767,31 +767,17 @@ int run_fp4_gemm(DevInfo* dev, const uint8_t* a, const uint8_t* b, const fp4::Ge
 
 // ---------------------------------------------------------------- masked attention
 
-int run_attention_few(DevInfo* dev, const MaskedParams& p, cudaStream_t st) {
-  constexpr auto kern = attention_few_kernel;
-  ZI_TRY((raise_smem<kern>(dev, int(few::kSmemBytes))));
-  const long long tiles = (static_cast<long long>(p.q_len) * p.group + 15) / 16;
-  const long long units = tiles * p.kv_heads * p.batch;
-  const int chunks = (p.kv_len + few::kChunk - 1) / few::kChunk;
-  int splits = 1;
-  while (splits < 8 && units * 2 * splits <= dev->sms && 2 * splits * few::kWarps <= chunks) splits *= 2;
-  if (tiles * splits > 0x7fffffffLL || p.kv_heads > 65535 || p.batch > 65535) return ZI_ERR_SHAPE;
-  return launch_clustered<kern>(ZI_KERNEL_ATTENTION_MASKED,
-                                dim3(unsigned(tiles * splits), unsigned(p.kv_heads), unsigned(p.batch)), few::kThreads,
-                                few::kSmemBytes, splits, st, p, splits);
-}
-
 // 4-D map over K or V: [batch][rows][heads][128] in any strides (those of size-1 dimensions are
-// not followed: any valid value), boxes of 64 columns x 128 rows of one head, 128-byte swizzle,
-// rows past the end zero.
+// not followed: any valid value), boxes of 64 columns x box_rows rows of one head, 128-byte
+// swizzle, rows past the end zero.
 int make_kv_map(CUtensorMap* m, const uint16_t* base, long long bs, long long rs, long long hs, int batch, int rows,
-                int heads) {
+                int heads, int box_rows) {
   EncodeTiledFn enc;
   if (encode_fn(&enc) != ZI_OK) return ZI_ERR_CUDA;
   const cuuint64_t dims[4] = {128, cuuint64_t(heads), cuuint64_t(rows), cuuint64_t(batch)};
   const cuuint64_t strides[3] = {cuuint64_t(hs ? hs * 2 : 256), cuuint64_t(rs ? rs * 2 : 256),
                                  cuuint64_t(bs ? bs * 2 : 256)};
-  const cuuint32_t box[4] = {64, 1, 128, 1};
+  const cuuint32_t box[4] = {64, 1, cuuint32_t(box_rows), 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t*>(base), dims, strides, box, estr,
                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -799,11 +785,28 @@ int make_kv_map(CUtensorMap* m, const uint16_t* base, long long bs, long long rs
   return r == CUDA_SUCCESS ? ZI_OK : ZI_ERR_CUDA;
 }
 
+int run_attention_few(DevInfo* dev, const MaskedParams& p, cudaStream_t st) {
+  CUtensorMap tk, tv;
+  ZI_TRY(make_kv_map(&tk, p.k, p.k_bs, p.k_rs, p.k_hs, p.batch, p.kv_len, p.kv_heads, few::kChunk));
+  ZI_TRY(make_kv_map(&tv, p.v, p.v_bs, p.v_rs, p.v_hs, p.batch, p.kv_len, p.kv_heads, few::kChunk));
+  constexpr auto kern = attention_few_kernel;
+  ZI_TRY((raise_smem<kern>(dev, int(few::kSmemBytes))));
+  const long long tiles = (static_cast<long long>(p.q_len) * p.group + 15) / 16;
+  const long long units = tiles * p.kv_heads * p.batch;
+  const int chunks = (p.kv_len + few::kChunk - 1) / few::kChunk;
+  int splits = 1;  // two CTAs per SM, at least two chunks per warp
+  while (splits < 8 && units * 2 * splits <= 2 * dev->sms && 4 * splits * few::kWarps <= chunks) splits *= 2;
+  if (tiles * splits > 0x7fffffffLL) return ZI_ERR_SHAPE;
+  return launch_clustered<kern>(ZI_KERNEL_ATTENTION_MASKED,
+                                dim3(unsigned(tiles * splits), unsigned(p.kv_heads), unsigned(p.batch)), few::kThreads,
+                                few::kSmemBytes, splits, st, tk, tv, p, splits);
+}
+
 template <bool CAP, bool BIAS>
 int run_attention_many(DevInfo* dev, const MaskedParams& p, cudaStream_t st) {
   CUtensorMap tk, tv;
-  ZI_TRY(make_kv_map(&tk, p.k, p.k_bs, p.k_rs, p.k_hs, p.batch, p.kv_len, p.kv_heads));
-  ZI_TRY(make_kv_map(&tv, p.v, p.v_bs, p.v_rs, p.v_hs, p.batch, p.kv_len, p.kv_heads));
+  ZI_TRY(make_kv_map(&tk, p.k, p.k_bs, p.k_rs, p.k_hs, p.batch, p.kv_len, p.kv_heads, 128));
+  ZI_TRY(make_kv_map(&tv, p.v, p.v_bs, p.v_rs, p.v_hs, p.batch, p.kv_len, p.kv_heads, 128));
   constexpr auto kern = attention_many_kernel<CAP, BIAS>;
   ZI_TRY((raise_smem<kern>(dev, int(many::kSmemBytes))));
   const long long x = (static_cast<long long>(p.q_len) * p.group + 255) / 256;
