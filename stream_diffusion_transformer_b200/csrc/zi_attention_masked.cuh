@@ -24,6 +24,7 @@ struct MaskedParams {
   const int* prefix;    // [batch] or null
   const int* lengths;   // [batch] or null
   const int *q_doc, *k_doc;  // [batch, q_len], [batch, kv_len], or null
+  int head_group;            // key heads whose units run side by side (attention_many_kernel)
 };
 
 // Keys of element b.
@@ -463,12 +464,18 @@ __global__ void __launch_bounds__(many::kThreads, 1)
   uint32_t* list = reinterpret_cast<uint32_t*>(smem + kList);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // Blocks: rank fastest, then the key heads (of all batch elements) of a group, then the 256-row units from the
+  // end: the longest ones (a causal mask's last rows, a pack's texts behind its images, which see several
+  // documents) start first.  Groups are as many heads as keep their K and V in L2 (p.head_group).
   const int rank = int(blockIdx.x) % splits;
-  const int units_x = int(gridDim.x) / splits;
-  const int unit = units_x - 1 - int(blockIdx.x) / splits;  // with a causal mask the last rows have the most keys: first
-  const int hk = blockIdx.y, b = blockIdx.z;
   const int rows = p.q_len * p.group;
-  const int row0 = unit * 256;
+  const int units = (rows + 255) / 256;
+  const int in_group = int(blockIdx.x) / splits % (units * p.head_group);
+  const int hb0 = int(blockIdx.x) / splits / (units * p.head_group) * p.head_group;
+  const int hb_n = min(p.head_group, p.kv_heads * p.batch - hb0);
+  const int hb = hb0 + in_group % hb_n;
+  const int hk = hb % p.kv_heads, b = hb / p.kv_heads;
+  const int row0 = (units - 1 - in_group / hb_n) * 256;
   const bool has_b = row0 + 128 < rows;
   const int n = masked_keys(p, b);
 
@@ -508,12 +515,21 @@ __global__ void __launch_bounds__(many::kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const bool skip = *abort_flag != 0;
 
-  // the row threads: what their row sees, and its Q to smem
+  // the row threads: their warp's 32 rows of Q to smem (half a warp per row, 256 contiguous bytes, all loads on
+  // their way at once), and what their own row sees
   const int row = row0 + int(threadIdx.x);
   const int qi = row / p.group, qg = row - qi * p.group;
   int lim = 0, doc = 0;
   if (warp < 8) {
     const bool have = row < rows;
+    const long long at = have ? b * p.q_bs + qi * p.q_rs + (hk * p.group + qg) * p.q_hs : -1;
+    const int x = lane & 15;
+    uint4 w[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const long long src = __shfl_sync(0xffffffffu, at, 2 * e + (lane >> 4));
+      w[e] = __ldg(reinterpret_cast<const uint4*>(p.q + (src < 0 ? 0 : src)) + x);
+    }
     int d_lo = 0x7fffffff, d_hi = -1, neg = 0;
     if (have) {
       lim = masked_limit(p, b, qi, n);
@@ -539,23 +555,12 @@ __global__ void __launch_bounds__(many::kThreads, 1)
       atomicMax(doc_max, d_hi);
       atomicMax(doc_neg, neg);
     }
-    // this warp's 32 rows of Q, half a warp per row (256 contiguous bytes)
-    const long long at = have ? b * p.q_bs + qi * p.q_rs + (hk * p.group + qg) * p.q_hs : -1;
-    const int x = lane & 15;
+    const int live = rows - (row0 + warp * 32);  // rows past the end are zeros
 #pragma unroll
-    for (int r0 = 0; r0 < 32; r0 += 16) {
-      uint4 w[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const long long src = __shfl_sync(0xffffffffu, at, r0 + 2 * e + (lane >> 4));
-        w[e] = src >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.q + src) + x) : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int i = (warp & 3) * 32 + r0 + 2 * e + (lane >> 4);
-        *reinterpret_cast<uint4*>(smem + kQ0 + (warp >> 2) * kTile + (x >> 3) * kHalf + i * 128 +
-                                  (((x & 7) ^ (i & 7)) << 4)) = w[e];
-      }
+    for (int e = 0; e < 16; ++e) {
+      const int r = 2 * e + (lane >> 4), i = (warp & 3) * 32 + r;
+      *reinterpret_cast<uint4*>(smem + kQ0 + (warp >> 2) * kTile + (x >> 3) * kHalf + i * 128 +
+                                (((x & 7) ^ (i & 7)) << 4)) = r < live ? w[e] : make_uint4(0, 0, 0, 0);
     }
     fence_proxy_async_smem();
   }
