@@ -384,9 +384,9 @@ __global__ void __launch_bounds__(few::kThreads)
 // - a row = one query of one head of a key head's group, packed as for few queries: the
 //   heads that share keys share the CTA's K and V tiles, and a causal tile spans fewer queries;
 // - Q written to smem by the row threads (any strides), K and V tiles by TMA;
-// - key tiles that no row of the CTA sees left out (by the rows' limits, and by the ranges of
-//   document ids of the tile and of the rows), elementwise masks only on tiles that some row
-//   sees in part;
+// - key tiles that no row of a row tile sees left out for it (by the rows' limits, and by the
+//   ranges of document ids of the key tile and of the rows), elementwise masks only on key
+//   tiles that some row sees in part;
 // - V rows that no query may see (past the element's keys, or with a negative id) cleared in
 //   smem before the product: zero probabilities times NaN would be NaN;
 // - with few CTAs, a cluster that shares a unit's keys and joins its partials through
@@ -399,9 +399,10 @@ constexpr uint32_t kTile = 128 * 128 * 2, kHalf = kTile / 2;
 constexpr int kKSlots = 3, kVSlots = 2;
 constexpr uint32_t kQ0 = 0, kK0 = 2 * kTile, kV0 = kK0 + kKSlots * kTile;
 constexpr uint32_t kBar = kV0 + kVSlots * kTile;
-constexpr int kListTiles = 4096;  // key tiles whose state fits the list (2 bits each); later ones are masked elementwise
+constexpr int kListTiles = 2048;  // key tiles whose state fits the lists; later ones are masked elementwise
+constexpr int kListWords = kListTiles / 16;  // of one row tile: 2 bits a key tile
 constexpr uint32_t kList = kBar + 256;
-constexpr uint32_t kSmemBytes = kList + kListTiles / 4 + 1024;
+constexpr uint32_t kSmemBytes = kList + 2 * kListWords * 4 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory");
 constexpr uint32_t kColS = 0, kColO = 256;
 // the partial of a split unit, over K and V: O [t][32 column quads][128 rows] float4, then (m, l) [256] float2
@@ -456,12 +457,12 @@ __global__ void __launch_bounds__(many::kThreads, 1)
   uint64_t* drain = bars + 18;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 19);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* lim_min = reinterpret_cast<int*>(tmem_slot + 2);
-  int* lim_max = lim_min + 1;
-  int* doc_min = lim_min + 2;  // of the rows' ids that are not negative ...
-  int* doc_max = lim_min + 3;
-  int* doc_neg = lim_min + 4;  // ... and whether any is
-  uint32_t* list = reinterpret_cast<uint32_t*>(smem + kList);
+  int* lim_min = reinterpret_cast<int*>(tmem_slot + 2);  // of the rows of tile A, of tile B (all arrays below likewise)
+  int* lim_max = lim_min + 2;
+  int* doc_min = lim_min + 4;  // of the rows' ids that are not negative ...
+  int* doc_max = lim_min + 6;
+  int* doc_neg = lim_min + 8;  // ... and whether any is
+  uint32_t* list = reinterpret_cast<uint32_t*>(smem + kList);  // [2][kListWords]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // Blocks: rank fastest, then the key heads (of all batch elements) of a group, then the 256-row units from the
@@ -476,7 +477,6 @@ __global__ void __launch_bounds__(many::kThreads, 1)
   const int hb = hb0 + in_group % hb_n;
   const int hk = hb % p.kv_heads, b = hb / p.kv_heads;
   const int row0 = (units - 1 - in_group / hb_n) * 256;
-  const bool has_b = row0 + 128 < rows;
   const int n = masked_keys(p, b);
 
   if (threadIdx.x == 0) {
@@ -494,11 +494,13 @@ __global__ void __launch_bounds__(many::kThreads, 1)
     }
     mbar_init(drain, 1);
     *abort_flag = device_error_set() ? 1 : 0;  // an earlier kernel timed out: leave everything untouched
-    *lim_min = 0x7fffffff;
-    *lim_max = 0;
-    *doc_min = 0x7fffffff;
-    *doc_max = -1;
-    *doc_neg = 0;
+    for (int t = 0; t < 2; ++t) {
+      lim_min[t] = 0x7fffffff;
+      lim_max[t] = 0;
+      doc_min[t] = 0x7fffffff;
+      doc_max[t] = -1;
+      doc_neg[t] = 0;
+    }
     fence_mbar_init();
   }
   if (warp == 8 && lane == 0) {
@@ -549,11 +551,12 @@ __global__ void __launch_bounds__(many::kThreads, 1)
     d_hi = __reduce_max_sync(0xffffffffu, d_hi);
     neg = __reduce_max_sync(0xffffffffu, neg);
     if (lane == 0) {
-      atomicMin(lim_min, lo);
-      atomicMax(lim_max, hi);
-      atomicMin(doc_min, d_lo);
-      atomicMax(doc_max, d_hi);
-      atomicMax(doc_neg, neg);
+      const int t = warp >> 2;
+      atomicMin(lim_min + t, lo);
+      atomicMax(lim_max + t, hi);
+      atomicMin(doc_min + t, d_lo);
+      atomicMax(doc_max + t, d_hi);
+      atomicMax(doc_neg + t, neg);
     }
     const int live = rows - (row0 + warp * 32);  // rows past the end are zeros
 #pragma unroll
@@ -565,16 +568,15 @@ __global__ void __launch_bounds__(many::kThreads, 1)
     fence_proxy_async_smem();
   }
   __syncthreads();
-  const int tiles = (*lim_max + 127) / 128;  // key tiles that any row of the CTA may see
-  const int all_lim = *lim_min;
+  const int tiles_a = (lim_max[0] + 127) / 128, tiles_b = (lim_max[1] + 127) / 128;  // key tiles that any of their rows may see
+  const int full_a = lim_min[0] / 128, full_b = lim_min[1] / 128;                    // ... that all see, by their limits
   const int* kd = p.k_doc ? p.k_doc + size_t(b) * p.kv_len : nullptr;
+  const int tiles = max(tiles_a, tiles_b);
   const int my_j0 = int(static_cast<long long>(rank) * tiles / splits);
   const int my_j1 = int(static_cast<long long>(rank + 1) * tiles / splits);
-  // tile states, 2 bits each, 16 tiles a word: 0 no row sees any key, 1 every row sees every key, 2 between
+  // key tile states per row tile, 2 bits each: 0 no row sees any key, 1 every row sees every key, 2 between
   if (kd) {
-    const int q_lo = *doc_min, q_hi = *doc_max;
-    const bool q_one = q_lo == q_hi && *doc_neg == 0;
-    for (int w = (my_j0 >> 4) + int(threadIdx.x); w * 16 < my_j1 && w < kListTiles / 16; w += kThreads) list[w] = 0;
+    for (int w = threadIdx.x; w < 2 * kListWords; w += kThreads) list[w] = 0;
     __syncthreads();
     constexpr int kWarps = kThreads / 32, kAhead = 3;  // tiles of ids in flight per warp
     for (int j = my_j0 + warp; j < my_j1 && j < kListTiles; j += kWarps * kAhead) {
@@ -599,24 +601,35 @@ __global__ void __launch_bounds__(many::kThreads, 1)
         lo = __reduce_min_sync(0xffffffffu, lo);
         hi = __reduce_max_sync(0xffffffffu, hi);
         neg = __reduce_max_sync(0xffffffffu, neg);
-        const bool none = hi < q_lo || lo > q_hi;
-        const bool full = q_one && !neg && lo == hi && lo == q_lo && (jj + 1) * 128 <= all_lim;
-        if (lane == 0 && !none && jj < my_j1 && jj < kListTiles) atomicOr(list + (jj >> 4), (full ? 1u : 2u) << (2 * (jj & 15)));
+        if (lane < 2 && jj < my_j1 && jj < kListTiles) {
+          const int t = lane;
+          const bool none = hi < doc_min[t] || lo > doc_max[t] || jj >= (t ? tiles_b : tiles_a);
+          const bool full = !neg && !doc_neg[t] && lo == hi && lo == doc_min[t] && lo == doc_max[t] &&
+                            jj < (t ? full_b : full_a);
+          if (!none) atomicOr(list + t * kListWords + (jj >> 4), (full ? 1u : 2u) << (2 * (jj & 15)));
+        }
       }
     }
     __syncthreads();
   }
-  auto state = [&](int j) -> uint32_t {
-    if (kd) return j < kListTiles ? (list[j >> 4] >> (2 * (j & 15))) & 3u : 2u;
-    return (j + 1) * 128 <= all_lim ? 1u : 2u;
+  auto state = [&](int t, int j) -> uint32_t {
+    if (j >= (t ? tiles_b : tiles_a)) return 0u;
+    if (kd) return j < kListTiles ? (list[t * kListWords + (j >> 4)] >> (2 * (j & 15))) & 3u : 2u;
+    return j < (t ? full_b : full_a) ? 1u : 2u;
   };
-  // the next tile of this CTA at or after j that some row sees (my_j1: none)
-  auto next = [&](int j) -> int {
-    if (kd)
-      while (j < my_j1 && state(j) == 0) ++j;
+  // the next key tile of this CTA at or after j that some row of the row tiles in `which` (bit 0 A, bit 1 B) sees;
+  // at or past my_j1: none
+  auto next = [&](int j, int which) -> int {
+    if (kd) {
+      while (j < my_j1 && j < kListTiles) {
+        const uint32_t w = ((which & 1 ? list[j >> 4] : 0u) | (which & 2 ? list[kListWords + (j >> 4)] : 0u)) >> (2 * (j & 15));
+        if (w) return j + (__ffs(w) - 1) / 2;
+        j = (j | 15) + 1;
+      }
+    }
     return j;
   };
-  const int first = skip ? my_j1 : next(my_j0);
+  const int first = skip ? my_j1 : next(my_j0, 3);
   const bool clean = p.lengths != nullptr || kd != nullptr;  // V may hold rows that nobody sees
 
   if (warp >= 8) {
@@ -631,7 +644,7 @@ __global__ void __launch_bounds__(many::kThreads, 1)
         const int nslots = kq ? kKSlots : kVSlots;
         int it = 0;
         bool ok = true;
-        for (int j = first; j < my_j1; j = next(j + 1), ++it) {
+        for (int j = first; j < my_j1; j = next(j + 1, 3), ++it) {
           const int bi = it % nslots;
           if (!mbar_wait(&emptyb[bi], (uint32_t(it / nslots) & 1u) ^ 1u, abort_flag, ZI_DEVERR_TIMEOUT_PRODUCER)) {
             ok = false;
@@ -648,13 +661,7 @@ __global__ void __launch_bounds__(many::kThreads, 1)
         }
       }
     } else if (warp == 9) {
-      int count = skip ? 0 : my_j1 - my_j0;  // tiles of this CTA that some row sees
-      if (kd && count > 0) {
-        count = 0;
-        for (int j = my_j0 + lane; j < my_j1; j += 32) count += state(j) != 0 ? 1 : 0;
-        count = __reduce_add_sync(0xffffffffu, count);
-      }
-      if (lane == 0 && count > 0) {
+if (lane == 0 && first < my_j1) {
         constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
         constexpr uint32_t idesc_o = idesc_bf16_f32(128, 128, false, true);
         auto issue_s = [&](int t, int it) {
@@ -667,14 +674,15 @@ __global__ void __launch_bounds__(many::kThreads, 1)
           }
           tc_commit(&s_full[t]);
         };
-        auto issue_pv = [&](int t, int it) -> bool {
-          if (!mbar_wait(&p_full[t], uint32_t(it) & 1u, abort_flag, ZI_DEVERR_TIMEOUT_MMA)) return false;
+        // done: products of tile t so far
+        auto issue_pv = [&](int t, int it, int done) -> bool {
+          if (!mbar_wait(&p_full[t], uint32_t(done) & 1u, abort_flag, ZI_DEVERR_TIMEOUT_MMA)) return false;
           tc_fence_after();
           const uint32_t v_low = desc_low(smem_u32(smem + kV0 + (it & 1) * kTile), kHalf);
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             tc_mma_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + 8 * k, desc_at(v_low, k * 2048), idesc_o,
-                      (it > 0 || k > 0) ? 1u : 0u);
+                      (done > 0 || k > 0) ? 1u : 0u);
           tc_commit(&pv_done[t]);
           return true;
         };
@@ -686,28 +694,36 @@ __global__ void __launch_bounds__(many::kThreads, 1)
           return mbar_wait(&v_full[it & 1], phase, abort_flag, ZI_DEVERR_TIMEOUT_MMA) &&
                  (!clean || mbar_wait(&v_clean[it & 1], phase, abort_flag, ZI_DEVERR_TIMEOUT_MMA));
         };
+        // S_A(0), S_B(0), then O_A += P_A(i) V, S_A(i + 1), O_B += P_B(i) V, S_B(i + 1), each tile where it sees the keys
+        bool need_a = state(0, first) != 0, need_b = state(1, first) != 0;
         bool ok = wait_k(0);
         if (ok) {
           tc_fence_after();
-          issue_s(0, 0);
-          if (has_b) issue_s(1, 0);
+          if (need_a) issue_s(0, 0);
+          if (need_b) issue_s(1, 0);
           tc_commit(&k_empty[0]);
-          ok = wait_v(0) && issue_pv(0, 0);
         }
-        for (int it = 0; it < count && ok; ++it) {
-          const bool more = it + 1 < count;
+        int it = 0, done_a = 0, done_b = 0;
+        for (int j = first; j < my_j1 && ok; ++it) {
+          const int nx = next(j + 1, 3);
+          const bool more = nx < my_j1;
+          const bool then_a = more && state(0, nx) != 0, then_b = more && state(1, nx) != 0;
+          if (!wait_v(it)) { ok = false; break; }
+          if (need_a && !issue_pv(0, it, done_a++)) { ok = false; break; }
           if (more) {
             if (!wait_k(it + 1)) { ok = false; break; }
             tc_fence_after();
-            issue_s(0, it + 1);
+            if (then_a) issue_s(0, it + 1);
           }
-          if (has_b && !issue_pv(1, it)) { ok = false; break; }
+          if (need_b && !issue_pv(1, it, done_b++)) { ok = false; break; }
           tc_commit(&v_empty[it & 1]);
           if (more) {
-            if (has_b) issue_s(1, it + 1);
+            if (then_b) issue_s(1, it + 1);
             tc_commit(&k_empty[(it + 1) % kKSlots]);
-            if (!wait_v(it + 1) || !issue_pv(0, it + 1)) { ok = false; break; }
           }
+          need_a = then_a;
+          need_b = then_b;
+          j = nx;
         }
         if (!ok) {
           tc_commit(drain);
@@ -717,9 +733,9 @@ __global__ void __launch_bounds__(many::kThreads, 1)
       }
     } else if (clean) {
       int it = 0;
-      for (int j = first; j < my_j1; j = next(j + 1), ++it) {
+      for (int j = first; j < my_j1; j = next(j + 1, 3), ++it) {
         uint32_t dirty = 0;  // bit e: nobody sees key j 128 + e 32 + lane
-        if (state(j) != 1) {
+        if (state(0, j) != 1 || state(1, j) != 1) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int key = j * 128 + e * 32 + lane;
@@ -761,7 +777,7 @@ __global__ void __launch_bounds__(many::kThreads, 1)
     float m_run = -INFINITY, l = 0.f;
     bool ok = !skip;
     int it = 0;
-    if (t == 0 || has_b) {
+    {
       // scores are in the exp2 domain after a cap, and scaled into it by the exponential's argument without one
       const float sl2 = CAP ? 1.f : p.scale_log2;
       float slope = 0.f, pos = 0.f;
@@ -782,8 +798,9 @@ __global__ void __launch_bounds__(many::kThreads, 1)
         cc[3] = -0.0337782849f * y1 * z2 * z2 * z2;
       }
       uint32_t s[128];
-      for (int j = first; ok && j < my_j1; j = next(j + 1), ++it) {
-        const bool part = state(j) != 1;
+      const int mine = 1 << t, stop = min(my_j1, t ? tiles_b : tiles_a);
+      for (int j = next(my_j0, mine); ok && j < stop; j = next(j + 1, mine)) {
+        const bool part = state(t, j) != 1;
         int id[4];  // document ids of keys w 32 + lane, on their way while S is computed
         if (kd && part) {
 #pragma unroll
@@ -936,6 +953,7 @@ __global__ void __launch_bounds__(many::kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[t]);  // for the whole warp: its stores are complete
+        ++it;
       }
       if (ok && it > 0) {
         ok = mbar_wait(&pv_done[t], uint32_t(it - 1) & 1u, abort_flag, ZI_DEVERR_TIMEOUT_SOFTMAX);
@@ -946,7 +964,7 @@ __global__ void __launch_bounds__(many::kThreads, 1)
     uint16_t* orow = p.out + b * p.o_bs + qi * p.o_rs + (hk * p.group + qg) * p.o_hs;
     if (splits == 1) {
       const float inv = m_run == -INFINITY ? 0.f : 1.0f / l;  // a row that sees no key: zeros
-      if (ok && (t == 0 || has_b)) {
+      if (ok) {
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t o[32];
@@ -964,14 +982,12 @@ __global__ void __launch_bounds__(many::kThreads, 1)
         }
       }
     } else {
-      // leave the partial in this CTA's smem (the rings are free: every load was consumed by an MMA that is done
-      // once both tiles' last product is) ...
-      if (ok && it > 0) {  // both tiles' products: the other tile may still read V
-        if (has_b) ok = mbar_wait(&pv_done[1 - t], uint32_t(it - 1) & 1u, abort_flag, ZI_DEVERR_TIMEOUT_SOFTMAX);
-      }
+      // leave the partial in this CTA's smem, once both tiles' last products are done: the rings are free then, every
+      // load was consumed by one ...
+      asm volatile("bar.sync 1, 256;" ::: "memory");
       float4* part = reinterpret_cast<float4*>(smem + kPart);
       float2* ml = reinterpret_cast<float2*>(smem + kPart + 2 * 32 * 128 * 16);
-      if (ok && (t == 0 || has_b)) {
+      if (ok) {
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t o[32];
@@ -991,7 +1007,7 @@ __global__ void __launch_bounds__(many::kThreads, 1)
       bool bad = false;
       for (int r = 0; r < splits; ++r)
         bad = bad || __float_as_int(ld_cluster_f32(smem_u32(const_cast<int*>(abort_flag)), r)) != 0;
-      if (!bad && live && (t == 0 || has_b)) {
+      if (!bad && live) {
         const uint32_t ml_addr = smem_u32(ml + t * 128 + i);
         float w[8], mm = -INFINITY, ll = 0.f;
 #pragma unroll
