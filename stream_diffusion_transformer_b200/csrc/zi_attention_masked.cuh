@@ -326,54 +326,88 @@ __global__ void __launch_bounds__(few::kThreads)
     }
   }
   __syncthreads();
-  // join the warps: thread d holds column d of every row
+  // join the warps, warps in order: 8 threads per row, 16 columns each
   float* cta = parts + kWarps * kPartFloats;
-  const int d = threadIdx.x;
   const int live = min(16, rows - row0);
-  for (int r = 0; r < live; ++r) {
-    float mm = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, parts[w * kPartFloats + 2048 + r]);
-    const float mu = mm == -INFINITY ? 0.f : mm;
-    float acc = 0.f, ll = 0.f;
+  if (int(threadIdx.x) / 8 < live) {
+    const int r = threadIdx.x / 8, x = threadIdx.x % 8;
+    float f[kWarps], mm = -INFINITY, ll = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float f = fast_exp2(parts[w * kPartFloats + 2048 + r] - mu);
-      acc = fmaf(f, parts[w * kPartFloats + r * 128 + d], acc);
-      ll = fmaf(f, parts[w * kPartFloats + 2064 + r], ll);
+      f[w] = parts[w * kPartFloats + 2048 + r];
+      mm = fmaxf(mm, f[w]);
     }
-    cta[r * 128 + d] = acc;
-    if (d == 0) {
+    const float mu = mm == -INFINITY ? 0.f : mm;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      f[w] = fast_exp2(f[w] - mu);
+      ll = fmaf(f[w], parts[w * kPartFloats + 2064 + r], ll);
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float4 y = *reinterpret_cast<const float4*>(parts + w * kPartFloats + r * 128 + (c * 8 + x) * 4);
+        acc = make_float4(fmaf(f[w], y.x, acc.x), fmaf(f[w], y.y, acc.y), fmaf(f[w], y.z, acc.z), fmaf(f[w], y.w, acc.w));
+      }
+      *reinterpret_cast<float4*>(cta + r * 128 + (c * 8 + x) * 4) = acc;
+    }
+    if (x == 0) {
       cta[2048 + r] = mm;
       cta[2064 + r] = ll;
     }
   }
   if (splits > 1) cluster_sync(); else __syncthreads();
-  // join the cluster: this CTA's share of the rows, ranks in order
+  // join the cluster, ranks in order: this CTA's share of the rows' 4-column pieces
+  const uint32_t cta_addr = smem_u32(cta), flag_addr = smem_u32(const_cast<int*>(abort_flag));
+  uint32_t peer[8];  // the ranks' shared memory (this CTA's own where there is no cluster)
   bool bad = false;
-  for (int w = 0; w < splits; ++w)
-    bad = bad || (splits > 1 ? __float_as_int(ld_cluster_f32(smem_u32(const_cast<int*>(abort_flag)), w)) : *abort_flag) != 0;
-  const uint32_t cta_addr = smem_u32(cta);
-  for (int r = rank; r < live && !bad; r += splits) {
-    float mm = -INFINITY, mw[8];
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    peer[w] = 0;
+    if (w < splits) {
+      uint32_t own, there = 0;
+      int f;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(own) : "r"(cta_addr), "r"(splits > 1 ? w : 0));
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(flag_addr), "r"(splits > 1 ? w : 0));
+      asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(f) : "r"(there) : "memory");
+      peer[w] = own;
+      bad = bad || f != 0;
+    }
+  }
+  auto ld1 = [](uint32_t addr) {
+    float x;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
+    return x;
+  };
+  for (int e = rank + int(threadIdx.x) * splits; e < live * 32 && !bad; e += kThreads * splits) {
+    const int r = e >> 5, c = e & 31;
+    float f[8], mm = -INFINITY, ll = 0.f;
 #pragma unroll
     for (int w = 0; w < 8; ++w) {
-      mw[w] = w >= splits ? -INFINITY : splits > 1 ? ld_cluster_f32(cta_addr + (2048 + r) * 4, w) : cta[2048 + r];
-      mm = fmaxf(mm, mw[w]);
+      f[w] = w < splits ? ld1(peer[w] + (2048 + r) * 4) : -INFINITY;
+      mm = fmaxf(mm, f[w]);
     }
     const float mu = mm == -INFINITY ? 0.f : mm;
-    float acc = 0.f, ll = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < 8; ++w) {
       if (w < splits) {
-        const float f = fast_exp2(mw[w] - mu);
-        acc = fmaf(f, splits > 1 ? ld_cluster_f32(cta_addr + (r * 128 + d) * 4, w) : cta[r * 128 + d], acc);
-        ll = fmaf(f, splits > 1 ? ld_cluster_f32(cta_addr + (2064 + r) * 4, w) : cta[2064 + r], ll);
+        f[w] = fast_exp2(f[w] - mu);
+        ll = fmaf(f[w], ld1(peer[w] + (2064 + r) * 4), ll);
+        float4 y;
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(y.x), "=f"(y.y), "=f"(y.z), "=f"(y.w)
+                     : "r"(peer[w] + (r * 128 + c * 4) * 4)
+                     : "memory");
+        acc = make_float4(fmaf(f[w], y.x, acc.x), fmaf(f[w], y.y, acc.y), fmaf(f[w], y.z, acc.z), fmaf(f[w], y.w, acc.w));
       }
     }
     const int row = row0 + r, i = row / p.group, g = row - i * p.group;
-    const __nv_bfloat16 yb = __float2bfloat16_rn(ll > 0.f ? acc / ll : 0.f);  // a row that sees no key: 0
-    p.out[b * p.o_bs + i * p.o_rs + (hk * p.group + g) * p.o_hs + d] = *reinterpret_cast<const uint16_t*>(&yb);
+    const float inv = ll > 0.f ? 1.f / ll : 0.f;  // a row that sees no key: 0
+    *reinterpret_cast<uint2*>(p.out + b * p.o_bs + i * p.o_rs + (hk * p.group + g) * p.o_hs + c * 4) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
   }
   if (splits > 1) cluster_sync();  // no CTA leaves while its partial may be read
 }

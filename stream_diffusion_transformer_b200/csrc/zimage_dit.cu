@@ -785,6 +785,25 @@ int make_kv_map(CUtensorMap* m, const uint16_t* base, long long bs, long long rs
   return r == CUDA_SUCCESS ? ZI_OK : ZI_ERR_CUDA;
 }
 
+// Cluster sizes: the keys of a unit are shared as long as every CTA still runs in the first wave and has a couple of
+// chunks per warp (few) or a key tile (many).  Two CTAs of the first kind fit an SM, but clusters leave some places
+// free: with 288 CTAs in clusters of 8 a second wave starts (6 key heads x 96 rows, 2,048 keys: 25 us, against
+// 17 us for 128 rows in clusters of 4).
+int few_splits(const DevInfo* dev, const MaskedParams& p) {
+  const long long units = (static_cast<long long>(p.q_len) * p.group + 15) / 16 * p.kv_heads * p.batch;
+  const int chunks = (p.kv_len + few::kChunk - 1) / few::kChunk;
+  int splits = 1;
+  while (splits < 8 && units * 2 * splits * 8 <= 14LL * dev->sms && 4 * splits * few::kWarps <= chunks) splits *= 2;
+  return splits;
+}
+int many_splits(const DevInfo* dev, const MaskedParams& p) {
+  const long long units = (static_cast<long long>(p.q_len) * p.group + 255) / 256 * p.kv_heads * p.batch;
+  const int tiles = (p.kv_len + 127) / 128;
+  int splits = 1;
+  while (splits < 8 && units * 2 * splits <= dev->sms && 2 * splits <= tiles) splits *= 2;
+  return splits;
+}
+
 int run_attention_few(DevInfo* dev, const MaskedParams& p, cudaStream_t st) {
   CUtensorMap tk, tv;
   ZI_TRY(make_kv_map(&tk, p.k, p.k_bs, p.k_rs, p.k_hs, p.batch, p.kv_len, p.kv_heads, few::kChunk));
@@ -792,10 +811,7 @@ int run_attention_few(DevInfo* dev, const MaskedParams& p, cudaStream_t st) {
   constexpr auto kern = attention_few_kernel;
   ZI_TRY((raise_smem<kern>(dev, int(few::kSmemBytes))));
   const long long tiles = (static_cast<long long>(p.q_len) * p.group + 15) / 16;
-  const long long units = tiles * p.kv_heads * p.batch;
-  const int chunks = (p.kv_len + few::kChunk - 1) / few::kChunk;
-  int splits = 1;  // two CTAs per SM, at least two chunks per warp
-  while (splits < 8 && units * 2 * splits <= 2 * dev->sms && 4 * splits * few::kWarps <= chunks) splits *= 2;
+  const int splits = few_splits(dev, p);
   if (tiles * splits > 0x7fffffffLL) return ZI_ERR_SHAPE;
   return launch_clustered<kern>(ZI_KERNEL_ATTENTION_MASKED,
                                 dim3(unsigned(tiles * splits), unsigned(p.kv_heads), unsigned(p.batch)), few::kThreads,
@@ -816,9 +832,7 @@ int run_attention_many(DevInfo* dev, MaskedParams p, cudaStream_t st) {
   ZI_TRY((raise_smem<kern>(dev, int(many::kSmemBytes))));
   const long long x = (static_cast<long long>(p.q_len) * p.group + 255) / 256;
   const long long units = x * p.kv_heads * p.batch;
-  const int tiles = (p.kv_len + 127) / 128;
-  int splits = 1;
-  while (splits < 8 && units * 2 * splits <= dev->sms && 4 * splits <= tiles) splits *= 2;
+  const int splits = many_splits(dev, p);
   if (units * splits > 0x7fffffffLL) return ZI_ERR_SHAPE;
   long long heads = kHeadGroupBytes / (512LL * p.kv_len);
   if (heads > static_cast<long long>(p.kv_heads) * p.batch) heads = static_cast<long long>(p.kv_heads) * p.batch;
@@ -827,9 +841,27 @@ int run_attention_many(DevInfo* dev, MaskedParams p, cudaStream_t st) {
                                 many::kSmemBytes, splits, st, tk, tv, p, splits);
 }
 
-// A step over a cache and the like (up to 16 rows per key head) is bound by reading K and V.
+// Which kernel: the one that a model of both, fitted on the B200 (1 to 128 rows per key head, 1 to 60 key heads,
+// 128 to 8,192 keys, all in one wave), says is faster.  In us:
+//   few   6.5 + the larger of 0.8 per chunk of its longest warp (loads of one warp in flight) and units x keys / 10,000
+//   many  9 (11 with a cluster) + 2.6 per key tile of a CTA
+// Measured few / many: 6 key heads x 64 rows, 8,192 keys 26.5 / 30.6, x 128 rows 42.1 / 31.4; 60 x 32 rows, 2,048
+// keys 25.8 / 32.4, x 48 rows 41.0 / 33.2.  Past 256 rows the second kernel's tiles are full.
+bool prefer_few(const DevInfo* dev, const MaskedParams& p) {
+  const long long rows = static_cast<long long>(p.q_len) * p.group, heads = static_cast<long long>(p.kv_heads) * p.batch;
+  if (rows > 256) return false;
+  const int fs = few_splits(dev, p), ms = many_splits(dev, p);
+  const double keys = p.kv_len;
+  const double chain = 0.8 * std::ceil(keys / (few::kChunk * few::kWarps * fs));
+  const double work = double((rows + 15) / 16 * heads) * keys / 10000.0;
+  const double few_us = 6.5 + (chain > work ? chain : work);
+  const double waves = std::ceil(double(heads) * ms / dev->sms);
+  const double many_us = (ms > 1 ? 11.0 : 9.0) + waves * 2.6 * std::ceil(keys / (128.0 * ms));
+  return few_us <= many_us;
+}
+
 int run_attention_masked(DevInfo* dev, const MaskedParams& p, cudaStream_t st) {
-  if (static_cast<long long>(p.q_len) * p.group <= 16) return run_attention_few(dev, p, st);
+  if (prefer_few(dev, p)) return run_attention_few(dev, p, st);
   if (p.cap_log2 != 0.f)
     return p.slopes ? run_attention_many<true, true>(dev, p, st) : run_attention_many<true, false>(dev, p, st);
   return p.slopes ? run_attention_many<false, true>(dev, p, st) : run_attention_many<false, false>(dev, p, st);
