@@ -20,7 +20,7 @@ LIB = os.path.join(PKG, "libzimage_dit.so")
 SOURCES = [os.path.join(PKG, "csrc", "zimage_dit.cu")]
 DEPS = SOURCES + [os.path.join(PKG, "csrc", f) for f in
                   ("zi_common.cuh", "zi_gemm.cuh", "zi_attention.cuh", "zi_rows.cuh",
-                   "zi_fp4.cuh", "zi_attention_masked.cuh")] + \
+                   "zi_cluster.cuh", "zi_fp4.cuh", "zi_attention_masked.cuh")] + \
        [os.path.join(ROOT, "include", "zimage_dit.h")]
 
 NVCC_FLAGS = [

@@ -7,6 +7,7 @@
 // ids are equal and not negative.
 #pragma once
 #include "zi_attention.cuh"
+#include "zi_cluster.cuh"
 #include "zi_common.cuh"
 
 namespace zi {
@@ -100,24 +101,6 @@ ZI_DEV void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-ZI_DEV float ld_cluster_f32(uint32_t addr, int rank) {
-  float x;
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(a) : "memory");
-  return x;
-}
-ZI_DEV float4 ld_cluster_f4(uint32_t addr, int rank) {
-  float4 x;
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
-               : "r"(a)
-               : "memory");
-  return x;
 }
 
 __global__ void __launch_bounds__(few::kThreads)
@@ -360,48 +343,33 @@ __global__ void __launch_bounds__(few::kThreads)
   }
   if (splits > 1) cluster_sync(); else __syncthreads();
   // join the cluster, ranks in order: this CTA's share of the rows' 4-column pieces
-  const uint32_t cta_addr = smem_u32(cta), flag_addr = smem_u32(const_cast<int*>(abort_flag));
-  uint32_t peer[8];  // the ranks' shared memory (this CTA's own where there is no cluster)
-  bool bad = false;
+  const bool bad = splits > 1 ? any_peer_set(abort_flag, splits) : *abort_flag != 0;
+  uint32_t peer[kMaxCluster];
 #pragma unroll
-  for (int w = 0; w < 8; ++w) {
-    peer[w] = 0;
-    if (w < splits) {
-      uint32_t own, there = 0;
-      int f;
-      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(own) : "r"(cta_addr), "r"(splits > 1 ? w : 0));
-      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(flag_addr), "r"(splits > 1 ? w : 0));
-      asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(f) : "r"(there) : "memory");
-      peer[w] = own;
-      bad = bad || f != 0;
-    }
-  }
-  auto ld1 = [](uint32_t addr) {
-    float x;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
-    return x;
-  };
+  for (int w = 0; w < kMaxCluster; ++w)
+    peer[w] = splits > 1 ? peer_addr(smem_u32(cta), w < splits ? w : 0) : smem_u32(cta);
   for (int e = rank + int(threadIdx.x) * splits; e < live * 32 && !bad; e += kThreads * splits) {
     const int r = e >> 5, c = e & 31;
-    float f[8], mm = -INFINITY, ll = 0.f;
+    float f[kMaxCluster], lw[kMaxCluster], mm = -INFINITY, ll = 0.f;
+    float4 y[kMaxCluster];
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
-      f[w] = w < splits ? ld1(peer[w] + (2048 + r) * 4) : -INFINITY;
-      mm = fmaxf(mm, f[w]);
+    for (int w = 0; w < kMaxCluster; ++w) {
+      f[w] = ld_peer(peer[w] + (2048 + r) * 4, w < splits);
+      lw[w] = ld_peer(peer[w] + (2064 + r) * 4, w < splits);
+      y[w] = ld_peer4(peer[w] + (r * 128 + c * 4) * 4, w < splits);
     }
+#pragma unroll
+    for (int w = 0; w < kMaxCluster; ++w)
+      if (w < splits) mm = fmaxf(mm, f[w]);
     const float mu = mm == -INFINITY ? 0.f : mm;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
+    for (int w = 0; w < kMaxCluster; ++w) {
       if (w < splits) {
         f[w] = fast_exp2(f[w] - mu);
-        ll = fmaf(f[w], ld1(peer[w] + (2064 + r) * 4), ll);
-        float4 y;
-        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                     : "=f"(y.x), "=f"(y.y), "=f"(y.z), "=f"(y.w)
-                     : "r"(peer[w] + (r * 128 + c * 4) * 4)
-                     : "memory");
-        acc = make_float4(fmaf(f[w], y.x, acc.x), fmaf(f[w], y.y, acc.y), fmaf(f[w], y.z, acc.z), fmaf(f[w], y.w, acc.w));
+        ll = fmaf(f[w], lw[w], ll);
+        acc = make_float4(fmaf(f[w], y[w].x, acc.x), fmaf(f[w], y[w].y, acc.y), fmaf(f[w], y[w].z, acc.z),
+                          fmaf(f[w], y[w].w, acc.w));
       }
     }
     const int row = row0 + r, i = row / p.group, g = row - i * p.group;
@@ -1038,33 +1006,33 @@ if (lane == 0 && first < my_j1) {
       __syncwarp();
       cluster_sync();
       // ... and join this rank's share of the columns of every row, ranks in order
-      bool bad = false;
-      for (int r = 0; r < splits; ++r)
-        bad = bad || __float_as_int(ld_cluster_f32(smem_u32(const_cast<int*>(abort_flag)), r)) != 0;
-      if (!bad && live) {
-        const uint32_t ml_addr = smem_u32(ml + t * 128 + i);
-        float w[8], mm = -INFINITY, ll = 0.f;
+      if (!any_peer_set(abort_flag, splits) && live) {
+        uint32_t peer[kMaxCluster];
+        float w[kMaxCluster], lw[kMaxCluster], mm = -INFINITY, ll = 0.f;
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          w[r] = r < splits ? ld_cluster_f32(ml_addr, r) : -INFINITY;
-          mm = fmaxf(mm, w[r]);
+        for (int r = 0; r < kMaxCluster; ++r) {
+          peer[r] = peer_addr(smem_u32(smem + kPart), r < splits ? r : 0);
+          const uint32_t at = peer[r] + 2 * 32 * 128 * 16 + (t * 128 + i) * 8;
+          w[r] = ld_peer(at, r < splits);
+          lw[r] = ld_peer(at + 4, r < splits);
         }
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          w[r] = w[r] == -INFINITY ? 0.f : fast_exp2(w[r] - mm);
-          if (r < splits && w[r] != 0.f) ll = fmaf(w[r], ld_cluster_f32(ml_addr + 4, r), ll);
+        for (int r = 0; r < kMaxCluster; ++r)
+          if (r < splits) mm = fmaxf(mm, w[r]);
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) {
+          w[r] = r >= splits || w[r] == -INFINITY ? 0.f : fast_exp2(w[r] - mm);
+          ll = fmaf(w[r], lw[r], ll);
         }
         const float inv = mm == -INFINITY ? 0.f : 1.0f / ll;
         for (int c = rank * 32 / splits; c < (rank + 1) * 32 / splits; ++c) {
-          const uint32_t addr = smem_u32(part + (t * 32 + c) * 128 + i);
+          float4 x[kMaxCluster];
+#pragma unroll
+          for (int r = 0; r < kMaxCluster; ++r) x[r] = ld_peer4(peer[r] + ((t * 32 + c) * 128 + i) * 16, r < splits);
           float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-          for (int r = 0; r < 8; ++r) {
-            if (r < splits) {
-              const float4 x = ld_cluster_f4(addr, r);
-              a = make_float4(fmaf(w[r], x.x, a.x), fmaf(w[r], x.y, a.y), fmaf(w[r], x.z, a.z), fmaf(w[r], x.w, a.w));
-            }
-          }
+          for (int r = 0; r < kMaxCluster; ++r)
+            a = make_float4(fmaf(w[r], x[r].x, a.x), fmaf(w[r], x[r].y, a.y), fmaf(w[r], x[r].z, a.z), fmaf(w[r], x[r].w, a.w));
           *reinterpret_cast<uint2*>(orow + 4 * c) =
               make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
         }

@@ -1,0 +1,52 @@
+// Reading the shared memory of a cluster's other CTAs.  The loads are predicated rather than
+// branched around, so that those of all ranks are on their way together.
+#pragma once
+#include "zi_common.cuh"
+
+namespace zi {
+
+constexpr int kMaxCluster = 8;
+
+// Address of this CTA's shared-memory offset `saddr` in CTA `rank` of the cluster.
+ZI_DEV uint32_t peer_addr(uint32_t saddr, int rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
+  return a;
+}
+
+// The value at a peer's address if `have`, else 0.
+ZI_DEV float ld_peer(uint32_t addr, bool have) {
+  float x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "mov.f32 %0, 0f00000000;\n\t"
+      "@p ld.shared::cluster.f32 %0, [%1];\n\t}"
+      : "=f"(x)
+      : "r"(addr), "r"(uint32_t(have))
+      : "memory");
+  return x;
+}
+ZI_DEV float4 ld_peer4(uint32_t addr, bool have) {
+  float4 x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %5, 0;\n\t"
+      "mov.f32 %0, 0f00000000;\n\tmov.f32 %1, 0f00000000;\n\tmov.f32 %2, 0f00000000;\n\tmov.f32 %3, 0f00000000;\n\t"
+      "@p ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+      : "r"(addr), "r"(uint32_t(have))
+      : "memory");
+  return x;
+}
+
+// Whether the 32-bit word at this CTA's offset is set in any of the cluster's first `ranks` CTAs.
+ZI_DEV bool any_peer_set(const volatile int* word, int ranks) {
+  const uint32_t saddr = smem_u32(const_cast<const int*>(word));
+  int f = 0;
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r) f |= __float_as_int(ld_peer(peer_addr(saddr, r < ranks ? r : 0), r < ranks));
+  return f != 0;
+}
+
+}  // namespace zi

@@ -12,6 +12,7 @@
 #include <cuda_fp4.h>
 
 #include "zi_attention.cuh"  // packed fp32 pairs
+#include "zi_cluster.cuh"
 #include "zi_common.cuh"
 #include "zi_gemm.cuh"
 
@@ -434,7 +435,7 @@ struct NarrowSmem {
   static constexpr uint32_t kA = TN * 128 < 1024 ? 1024 : TN * 128;
   static constexpr uint32_t kSc = kStageTiles<FMT> * kTileBytes;  // scales of one operand
   static constexpr uint32_t kStage = kB + kA + 2 * kSc;
-  static constexpr int kStages = TN <= 32 ? 4 : 5;
+  static constexpr int kStages = TN <= 32 ? 4 : 3;              // two CTAs per SM
   static constexpr uint32_t kBar = kStages * kStage;
   static constexpr uint32_t kBytes = kBar + 256 + 1024;
   static constexpr uint32_t kCols = TN <= 32 ? 128 : 256;         // TMEM: D, then two scale buffers
@@ -442,6 +443,7 @@ struct NarrowSmem {
   static constexpr uint32_t kScaleCols = 2 * 4 * kStageTiles<FMT>;  // B's and A's, per buffer
   static_assert(kColScale + 2 * kScaleCols <= kCols, "TMEM columns");
   static_assert(kStage % 1024 == 0 && 128 * TN * 4 <= kBar, "stage alignment; the partial fits the ring");
+  static_assert(2 * (kBytes + 1024) <= 233472, "two CTAs per SM");
 };
 
 template <int FMT, int TN>
@@ -572,40 +574,38 @@ __global__ void __launch_bounds__(kNarrowThreads)
     }
   }
   if (splits > 1) cluster_sync(); else __syncthreads();
-  // this CTA's share of the tile's TN columns, summed over the ranks in order
-  const int c0 = rank * TN / splits, c1 = (rank + 1) * TN / splits;
-  bool bad = *abort_flag != 0;
-  const uint32_t base = smem_u32(part), flag = smem_u32(const_cast<int*>(abort_flag));
-  if (splits > 1) {
-    for (int r = 0; r < splits; ++r) {
-      uint32_t addr, f;
-      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(flag), "r"(r));
-      asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(f) : "r"(addr) : "memory");
-      bad = bad || f != 0;
-    }
-  }
-  const int pair = int(threadIdx.x) & 63;  // two neighbouring output columns
-  const int n = n0 + 2 * pair;
-  if (!bad && n < p.N) {  // N is even
-    const float s0 = p.brs ? __ldg(p.brs + n) : 1.f, s1 = p.brs ? __ldg(p.brs + n + 1) : 1.f;
-    for (int c = c0 + int(threadIdx.x >> 6); c < c1; c += kNarrowThreads / 64) {
-      const int m = m0 + c;
-      if (m >= p.M) break;
-      float x = 0.f, y = 0.f;
-      for (int r = 0; r < splits; ++r) {
-        float u, w;
-        uint32_t addr = base + uint32_t(c * 128 + 2 * pair) * 4;
-        if (splits > 1) {
-          asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(addr), "r"(r));
-          asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(u), "=f"(w) : "r"(addr) : "memory");
-        } else {
-          asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(u), "=f"(w) : "r"(addr) : "memory");
-        }
-        x += u;
-        y += w;
+  // this CTA's share of the tile's rows of A, summed over the ranks in order: a warp per row, 4 columns of the output
+  // per thread, two rows at a time
+  const bool bad = splits > 1 ? any_peer_set(abort_flag, splits) : *abort_flag != 0;
+  const int c0 = rank * TN / splits, c1 = min((rank + 1) * TN / splits, p.M - m0);
+  const int n = n0 + 4 * lane;
+  if (!bad && n < p.N) {  // N is a multiple of 8
+    uint32_t peer[kMaxCluster];
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r)
+      peer[r] = splits > 1 ? peer_addr(smem_u32(part) + 16 * lane, r < splits ? r : 0) : smem_u32(part) + 16 * lane;
+    const float4 rb = p.brs ? __ldg(reinterpret_cast<const float4*>(p.brs + n)) : make_float4(1.f, 1.f, 1.f, 1.f);
+    constexpr int kWarps = kNarrowThreads / 32;
+    for (int c = c0 + warp; c < c1; c += 2 * kWarps) {
+      float4 v[2][kMaxCluster];
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) {
+        v[0][r] = ld_peer4(peer[r] + c * 512, r < splits);
+        v[1][r] = ld_peer4(peer[r] + (c + kWarps) * 512, r < splits && c + kWarps < c1);
       }
-      const float a = p.ars ? __ldg(p.ars + m) : 1.f;
-      *reinterpret_cast<uint32_t*>(p.out + size_t(m) * p.N + n) = pack_bf16x2(x * (a * s0), y * (a * s1));
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int m = m0 + c + u * kWarps;
+        if (c + u * kWarps < c1) {
+          float4 x = v[u][0];
+#pragma unroll
+          for (int r = 1; r < kMaxCluster; ++r)
+            if (r < splits) x = make_float4(x.x + v[u][r].x, x.y + v[u][r].y, x.z + v[u][r].z, x.w + v[u][r].w);
+          const float ra = p.ars ? __ldg(p.ars + m) : 1.f;
+          *reinterpret_cast<uint2*>(p.out + size_t(m) * p.N + n) =
+              make_uint2(pack_bf16x2(x.x * (ra * rb.x), x.y * (ra * rb.y)), pack_bf16x2(x.z * (ra * rb.z), x.w * (ra * rb.w)));
+        }
+      }
     }
   }
   if (splits > 1) cluster_sync(); else __syncthreads();  // no CTA leaves while its partial may be read

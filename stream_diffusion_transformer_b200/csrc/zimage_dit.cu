@@ -711,7 +711,7 @@ int run_fp4_narrow(DevInfo* dev, const uint8_t* a, const uint8_t* b, const fp4::
   if (mt > 65535) return ZI_ERR_SHAPE;
   const int stages = (p.K + fp4::kStageK - 1) / fp4::kStageK;
   int splits = 1;
-  while (splits < 8 && 2 * splits <= stages && static_cast<long long>(nt) * mt * 2 * splits <= dev->sms) splits *= 2;
+  while (splits < 8 && 2 * splits <= stages && static_cast<long long>(nt) * mt * 2 * splits * 8 <= 14LL * dev->sms) splits *= 2;
   return launch_clustered<kern>(ZI_KERNEL_GEMM_FP4, dim3(unsigned(nt * splits), unsigned(mt)), fp4::kNarrowThreads,
                                 L::kBytes, splits, st, ta, tb, p, splits);
 }
@@ -756,12 +756,17 @@ int run_fp4_wide(DevInfo* dev, const uint8_t* a, const uint8_t* b, const fp4::Ge
   return launched(ZI_KERNEL_GEMM_FP4, st);
 }
 
+// Up to 64 rows of A the narrow kernel's tiles fit the rows; past that it is taken while its 128 x 128 tiles are
+// about one per SM (each B row is read for every 128 rows of A), the pair kernel for more.  Measured narrow / wide in
+// us, NVFP4, K = 3840: 64 rows x 20480 20.8 / 28.0; 128 x 20480 (160 tiles) 25.3 / 30.0; 512 x 3840 (120) 17.1 / 18.1;
+// 256 x 11520 (180) 24.9 / 18.4; 768 x 3840 (180) 24.2 / 18.4.
 template <int FMT>
 int run_fp4_gemm(DevInfo* dev, const uint8_t* a, const uint8_t* b, const fp4::GemmParams& p, cudaStream_t st) {
   if (p.M <= 16) return run_fp4_narrow<FMT, 16>(dev, a, b, p, st);
   if (p.M <= 32) return run_fp4_narrow<FMT, 32>(dev, a, b, p, st);
   if (p.M <= 64) return run_fp4_narrow<FMT, 64>(dev, a, b, p, st);
-  if (p.M <= 512) return run_fp4_narrow<FMT, 128>(dev, a, b, p, st);
+  const long long tiles = static_cast<long long>((p.M + 127) / 128) * ((p.N + 127) / 128);
+  if (8 * tiles <= 9LL * dev->sms) return run_fp4_narrow<FMT, 128>(dev, a, b, p, st);
   return run_fp4_wide<FMT>(dev, a, b, p, st);
 }
 
