@@ -122,6 +122,24 @@ typedef struct zi_block_weights {
   const float* s_out;      /* [D] */
   const uint8_t* w2_8;     /* [D, Fp] e4m3 codes of w2 (zero columns F..Fp) */
   const float* s_2;        /* [D] */
+  /* Optional 4-bit projections (zi_quantize_fp4 of the same matrices; not beside e4m3
+   * ones): codes, block scales and, for NVFP4, row scales (all row scales NULL means
+   * MXFP4).  QKV and w1|w3 (or none), then optionally the output projection and w2 too.
+   * The rows going into each are brought to 4 bits by a pass before it; the products run
+   * on the tensor cores in kind::mxf4nvf4 with the same fused epilogues.  Blocks in 4 bits
+   * and in bf16 may stand in one model. */
+  const uint8_t* w_qkv4;   /* [3D, D / 2] codes ... */
+  const uint8_t* b_qkv4;   /* block scales ... */
+  const float* r_qkv4;     /* [3D] row scales, or NULL */
+  const uint8_t* w13_4;    /* [2Fp, D / 2] */
+  const uint8_t* b_13_4;
+  const float* r_13_4;     /* [2Fp] */
+  const uint8_t* w_out4;   /* [D, D / 2] */
+  const uint8_t* b_out4;
+  const float* r_out4;     /* [D] */
+  const uint8_t* w2_4;     /* [D, Fp / 2]; Fp <= 16384 */
+  const uint8_t* b_2_4;
+  const float* r_2_4;      /* [D] */
 } zi_block_weights;
 
 /* Weights of the whole transformer.  The block arrays are HOST arrays (of

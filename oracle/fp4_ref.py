@@ -81,3 +81,51 @@ def tile_scales(stored):
     i, j = np.meshgrid(np.arange(R), np.arange(nb), indexing="ij")
     out[((i // 128) * tx + j // 4) * 512 + (i % 32) * 16 + (i % 128) // 32 * 4 + j % 4] = stored
     return out
+
+
+def rows_values(x, fmt):
+    """What the rows of x stand for after a round trip through the format."""
+    return dequantize(*quantize(x, fmt), fmt)
+
+
+def fp4_linear(h, w, fmt):
+    """h [M, K] @ w [N, K]^T with both operands in 4 bits."""
+    return rows_values(h, fmt) @ rows_values(w, fmt).T
+
+
+def block_forward(x, W, prefix, d, angles, c=None, fmt="nvfp4", all=False):
+    """The block of zimage_ref.block_forward with the QKV and FFN w1|w3 projections in 4 bits (all=True: the
+    output projection and FFN w2 as well); what goes into each is rounded to bf16 first, as the GPU holds it."""
+    from . import zimage_ref as ref
+
+    def lin(h, w, four=True):
+        return fp4_linear(to_bf16(h), w, fmt) if four else ref.linear(h, w)
+
+    S, D = x.shape
+    if c is not None:
+        scale_msa, gate_msa, scale_mlp, gate_mlp = ref.adaln(c, W, prefix)
+    else:
+        scale_msa = scale_mlp = 0.0
+        gate_msa = gate_mlp = 1.0
+    a, ff = f"{prefix}.attention", f"{prefix}.feed_forward"
+    h = ref.rms_norm(x, W(f"{prefix}.attention_norm1.weight")) * (1.0 + scale_msa)
+    q, k, v = (lin(h, W(f"{a}.{n}.weight")).reshape(S, d.heads, d.head_dim) for n in ("to_q", "to_k", "to_v"))
+    q = ref.apply_rope(ref.rms_norm(q, W(f"{a}.norm_q.weight")), angles)
+    k = ref.apply_rope(ref.rms_norm(k, W(f"{a}.norm_k.weight")), angles)
+    o = lin(ref.attention(q, k, v).reshape(S, D), W(f"{a}.to_out.weight"), all)
+    x1 = x + gate_msa * ref.rms_norm(o, W(f"{prefix}.attention_norm2.weight"))
+    h2 = ref.rms_norm(x1, W(f"{prefix}.ffn_norm1.weight")) * (1.0 + scale_mlp)
+    u = ref.silu(lin(h2, W(f"{ff}.w1.weight"))) * lin(h2, W(f"{ff}.w3.weight"))
+    if u.shape[1] % 32 and all:
+        pad = -u.shape[1] % 128  # zero columns, as the library pads them
+        f = lin(np.pad(u, ((0, 0), (0, pad))), np.pad(W(f"{ff}.w2.weight"), ((0, 0), (0, pad))))
+    else:
+        f = lin(u, W(f"{ff}.w2.weight"), all)
+    return x1 + gate_mlp * ref.rms_norm(f, W(f"{prefix}.ffn_norm2.weight"))
+
+
+def to_bf16(x):
+    """x rounded to bf16 (nearest even), as fp64."""
+    u = np.asarray(x, dtype=np.float32).view(np.uint32)
+    u = (u + 0x7FFF + ((u >> 16) & 1)) & np.uint32(0xFFFF0000)
+    return u.view(np.float32).astype(np.float64)

@@ -35,7 +35,9 @@ class ZiConfig(ctypes.Structure):
 
 
 BLOCK_FIELDS = ("w_qkv", "w_out", "w13", "w2", "g_attn1", "g_attn2", "g_ffn1", "g_ffn2", "g_q", "g_k",
-                "w_ada", "b_ada", "w_qkv8", "s_qkv", "w13_8", "s_13", "w_out8", "s_out", "w2_8", "s_2")
+                "w_ada", "b_ada", "w_qkv8", "s_qkv", "w13_8", "s_13", "w_out8", "s_out", "w2_8", "s_2",
+                "w_qkv4", "b_qkv4", "r_qkv4", "w13_4", "b_13_4", "r_13_4", "w_out4", "b_out4", "r_out4", "w2_4",
+                "b_2_4", "r_2_4")
 
 
 class ZiBlockWeights(ctypes.Structure):

@@ -685,11 +685,76 @@ ZI_DEV void tmem_st4(uint32_t taddr, uint4 w) {
                : "memory");
 }
 
-template <int FMT>
+// The epilogue of one row's 128 accumulator columns, in registers: `half` 0 or 1 of the 256-wide tile at
+// column n0 (EPI_SWIGLU: v[0..63] gate columns n0 + 64 half, v[64..127] their up columns 128 further).  The
+// fused forms are those of gemm_epilogue: EPI_QKV one head, EPI_SWIGLU 64 outputs.
+template <int FMT, int EPI>
+ZI_DEV void wide_epilogue(uint32_t* v, int m, int n0, int half, const GemmParams& p, const EpiParams& ep) {
+  static_assert(EPI == EPI_BF16 || EPI == EPI_QKV || EPI == EPI_SWIGLU, "epilogues of the 4-bit product");
+  const int nb = n0 + half * 128;
+  if constexpr (FMT == NV) {
+    const float ra = __ldg(p.ars + m);
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {  // 8 columns; N is a multiple of 8
+      const int col = EPI == EPI_SWIGLU ? n0 + 64 * half + 8 * c + (c >= 8 ? 64 : 0) : nb + 8 * c;
+      if (EPI != EPI_BF16 || col < p.N) {
+        const float4* bs = reinterpret_cast<const float4*>(p.brs + col);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float4 w = __ldg(bs + h);
+          uint32_t* x = v + 8 * c + 4 * h;
+          x[0] = __float_as_uint(__uint_as_float(x[0]) * (ra * w.x));
+          x[1] = __float_as_uint(__uint_as_float(x[1]) * (ra * w.y));
+          x[2] = __float_as_uint(__uint_as_float(x[2]) * (ra * w.z));
+          x[3] = __float_as_uint(__uint_as_float(x[3]) * (ra * w.w));
+        }
+      }
+    }
+  }
+  auto f = [&](int i) { return __uint_as_float(v[i]); };
+  if constexpr (EPI == EPI_SWIGLU) {
+    uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(ep.out) + size_t(m) * ep.ldo + n0 / 2 + 64 * half);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = f(8 * c + i) / (1.0f + __expf(-f(8 * c + i))) * f(64 + 8 * c + i);
+      out[c] = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+    }
+    return;
+  }
+  uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(ep.out) + size_t(m) * ep.ldo + nb);
+  if constexpr (EPI == EPI_QKV) {
+    const int region = n0 / ep.dim;  // 0 = q, 1 = k, 2 = v
+    if (region < 2) {
+      const uint16_t* g = region == 0 ? ep.g_q : ep.g_k;
+      const float2* rp = ep.rope + ep.map.tab(m + ep.row_off);  // pair j at rp[j * rope_n]
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < 128; ++i) ss = fmaf(f(i), f(i), ss);
+      const float r = rsqrtf(ss * (1.0f / 128.0f) + ep.eps);
+#pragma unroll
+      for (int i = 0; i < 64; ++i) {
+        const uint32_t gp = __ldg(reinterpret_cast<const uint32_t*>(g) + i);  // gains of dims 2i, 2i + 1
+        const float a = f(2 * i) * r * __uint_as_float(gp << 16), b = f(2 * i + 1) * r * __uint_as_float(gp & 0xFFFF0000u);
+        const float2 cs = __ldg(rp + size_t(i) * ep.rope_n);
+        v[2 * i] = __float_as_uint(a * cs.x - b * cs.y);
+        v[2 * i + 1] = __float_as_uint(a * cs.y + b * cs.x);
+      }
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < 16; ++c)
+    if (EPI != EPI_BF16 || nb + 8 * c < p.N)
+      out[c] = make_uint4(pack_bf16x2(f(8 * c), f(8 * c + 1)), pack_bf16x2(f(8 * c + 2), f(8 * c + 3)),
+                          pack_bf16x2(f(8 * c + 4), f(8 * c + 5)), pack_bf16x2(f(8 * c + 6), f(8 * c + 7)));
+}
+
+template <int FMT, int EPI>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
     gemm_wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB, GemmParams p,
-                     TailSched sched) {
+                     EpiParams ep, TailSched sched) {
   using L = WideSmem<FMT>;
   constexpr int kStages = L::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -854,7 +919,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
       tc_fence_after();
       uint32_t v[128];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(tmem + (uint32_t(q * 32) << 16) + half * 128 + c * 32, &v[c * 32]);
+      for (int c = 0; c < 4; ++c)
+        tmem_ld32(tmem + (uint32_t(q * 32) << 16) +
+                      (EPI == EPI_SWIGLU ? half * 64 + c * 32 + (c >= 2 ? 64 : 0) : half * 128 + c * 32),
+                  &v[c * 32]);
       tmem_wait_ld();
 #pragma unroll
       for (int c = 0; c < 4; ++c) reg_fence32(&v[c * 32]);
@@ -863,32 +931,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
       if (lane == 0) mbar_arrive_leader(tempty);
       int m0, n0;
       tile_origin<256, 256>(sched, num_m, wi.tile, m0, n0);
-      const int m = m0 + 128 * int(rank) + q * 32 + lane, nb = n0 + half * 128;
-      if (m < p.M) {
-        const float ra = FMT == NV ? __ldg(p.ars + m) : 1.f;
-        uint16_t* out = p.out + size_t(m) * p.N + nb;
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {  // 8 columns; N is a multiple of 8
-          if (nb + 8 * c < p.N) {
-            float f[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[8 * c + i]);
-            if constexpr (FMT == NV) {
-              const float4* bs = reinterpret_cast<const float4*>(p.brs + nb + 8 * c);
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const float4 w = __ldg(bs + h);
-                f[4 * h] *= ra * w.x;
-                f[4 * h + 1] *= ra * w.y;
-                f[4 * h + 2] *= ra * w.z;
-                f[4 * h + 3] *= ra * w.w;
-              }
-            }
-            *reinterpret_cast<uint4*>(out + 8 * c) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                                                                pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
-          }
-        }
-      }
+      const int m = m0 + 128 * int(rank) + q * 32 + lane;
+      if (m < p.M) wide_epilogue<FMT, EPI>(v, m, n0, half, p, ep);
     }
   }
 

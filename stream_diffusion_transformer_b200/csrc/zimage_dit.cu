@@ -324,294 +324,6 @@ int run_attention(DevInfo* dev, const uint16_t* qkv, int qkv_rows, uint16_t* out
   return launched(ZI_KERNEL_ATTENTION, st);
 }
 
-// ---------------------------------------------------------------- row kernels
-
-// hq non-null: the output is e4m3 codes [rows][D] with per-row scales hs instead of bf16 h.
-template <typename TIn>
-int run_rms_mod(const TIn* x, int rows, int D, const uint16_t* gain, const float* scale, int scale_ld, RowMap map,
-                int row_off, float eps, uint16_t* h, cudaStream_t st, uint8_t* hq = nullptr, float* hs = nullptr) {
-  if (rows <= 0) return ZI_OK;
-  prof_pre(st);
-  rms_mod_kernel<TIn><<<rows, kRowThreads, 0, st>>>(x, D, gain, scale, scale_ld, map, row_off, eps, h, hq, hs);
-  return launched(ZI_KERNEL_PRE_NORM, st);
-}
-
-// Per-row e4m3 codes and scales of a [rows, cols] fp32 or bf16 matrix (cols <= 16384).
-constexpr int kQuantMaxCols = kRowThreads * 16 * 4;
-template <typename TIn>
-int run_quantize(const TIn* x, int rows, int cols, uint8_t* q, float* sc, cudaStream_t st) {
-  if (rows <= 0) return ZI_OK;
-  prof_pre(st);
-  if (cols <= kRowThreads * kRowMaxVec * 4)
-    quantize_rows_e4m3_kernel<TIn, kRowMaxVec><<<rows, kRowThreads, 0, st>>>(x, cols, q, sc);
-  else
-    quantize_rows_e4m3_kernel<TIn, 16><<<rows, kRowThreads, 0, st>>>(x, cols, q, sc);
-  return launched(ZI_KERNEL_QUANTIZE, st);
-}
-
-int run_post(const PostParams& p, int rows, cudaStream_t st) {
-  if (rows <= 0) return ZI_OK;
-  prof_pre(st);
-  post_residual_kernel<<<rows, kRowThreads, 0, st>>>(p);
-  return launched(ZI_KERNEL_POST_NORM, st);
-}
-
-// ---------------------------------------------------------------- workspace
-
-constexpr size_t kAlign = 1024;
-inline size_t up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
-
-struct Ws {
-  size_t mod, c, silu, hid, lens, pos, rope, x, h, hs, qkv, att, o, u, q8, q8s, tok, capn, split_cnt, split_part,
-      total;
-};
-
-Ws carve(const zi_config& cfg, int batch, int s_img, int s_txt, bool model, int mod_cols) {
-  const size_t D = size_t(cfg.dim);
-  const size_t S = size_t(s_img) + size_t(s_txt);
-  const size_t rows = size_t(batch) * S;
-  const size_t Fp = size_t(zi_ffn_padded(cfg.ffn));
-  const size_t pairs = size_t(cfg.head_dim) / 2;
-  Ws w;
-  size_t o = 0;
-  w.mod = o; o = up(o + size_t(batch) * size_t(mod_cols) * 4);
-  w.c = o; o = up(o + (model ? size_t(batch) * 256 * 4 : 0));
-  w.silu = o; o = up(o + (model ? size_t(batch) * 256 * 4 : 0));
-  w.hid = o; o = up(o + (model ? size_t(batch) * size_t(cfg.t_mid) * 4 : 0));
-  // a model forward may give every batch element its own positions (text lengths)
-  const size_t tab_rows = model ? rows : S;
-  w.lens = o; o = up(o + (model ? size_t(batch) * 4 : 0));
-  w.pos = o; o = up(o + (model ? tab_rows * 3 * 4 : 0));
-  w.rope = o; o = up(o + tab_rows * pairs * 8);
-  w.x = o; o = up(o + (model ? rows * D * 4 : 0));
-  w.h = o; o = up(o + rows * D * 2);  // bf16 h, or e4m3 codes (rows x D bytes) for e4m3 blocks
-  w.hs = o; o = up(o + rows * 4);      // per-row scales of e4m3 h
-  w.qkv = o; o = up(o + rows * 3 * D * 2);
-  w.att = o; o = up(o + rows * D * 2);
-  w.o = o; o = up(o + rows * D * 2);
-  w.u = o; o = up(o + rows * Fp * 2);
-  // e4m3 codes of the attention output or of u (never live together) and their row scales
-  w.q8 = o; o = up(o + rows * (Fp > D ? Fp : D));
-  w.q8s = o; o = up(o + rows * 4);
-  w.tok = o; o = up(o + (model ? size_t(batch) * s_img * size_t(4 * cfg.in_ch) * 2 : 0));
-  w.capn = o; o = up(o + (model ? size_t(batch) * s_txt * size_t(cfg.cap_dim) * 2 : 0));
-  w.split_cnt = o; o = up(o + size_t(kSplitSlots) * 4);
-  w.split_part = o; o = up(o + size_t(kSplitSlots) * kSplitSlotBytes);
-  w.total = o;
-  return w;
-}
-
-int check_cfg(const zi_config* c) {
-  if (!c) return ZI_ERR_ARG;
-  if (c->head_dim != 128 || c->patch != 2) return ZI_ERR_SHAPE;
-  if (c->dim <= 0 || c->dim % 256 != 0 || c->dim != c->heads * c->head_dim || c->dim > 4096) return ZI_ERR_SHAPE;
-  if (c->rope_axes[0] + c->rope_axes[1] + c->rope_axes[2] != c->head_dim) return ZI_ERR_SHAPE;
-  for (int i = 0; i < 3; ++i)
-    if (c->rope_axes[i] <= 0 || c->rope_axes[i] % 2) return ZI_ERR_SHAPE;
-  if (c->ffn <= 0 || c->cap_dim <= 0 || c->cap_dim % 64 != 0 || c->cap_dim > 4096) return ZI_ERR_SHAPE;
-  if (c->t_freq != 256 || c->t_mid <= 0 || c->t_mid % 8) return ZI_ERR_SHAPE;  // warp-per-row timestep MLP
-  if ((c->dim < 256 ? c->dim : 256) != 256) return ZI_ERR_SHAPE;  // adaLN GEMV is 256 wide
-  if (4 * c->in_ch != 64) return ZI_ERR_SHAPE;                     // final linear uses a 64-wide tile
-  if (c->n_noise < 0 || c->n_ctx < 0 || c->n_main < 1 || c->n_noise + c->n_main + 1 > kMaxAdaSegs)
-    return ZI_ERR_SHAPE;
-  return ZI_OK;
-}
-
-bool block_ptrs_ok(const zi_block_weights* w, bool need_mod) {
-  if (!w) return false;
-  const void* ps[] = {w->w_qkv, w->w_out, w->w13, w->w2, w->g_attn1, w->g_attn2, w->g_ffn1, w->g_ffn2, w->g_q, w->g_k};
-  for (const void* p : ps)
-    if (!p) return false;
-  if (need_mod && (!w->w_ada || !w->b_ada)) return false;
-  if ((w->w_ada == nullptr) != (w->b_ada == nullptr)) return false;
-  // e4m3 projections: all four of w_qkv8, s_qkv, w13_8, s_13, or none; then optionally
-  // all four of w_out8, s_out, w2_8, s_2
-  const int nf8 = (w->w_qkv8 != nullptr) + (w->s_qkv != nullptr) + (w->w13_8 != nullptr) + (w->s_13 != nullptr);
-  if (nf8 != 0 && nf8 != 4) return false;
-  const int nf8b = (w->w_out8 != nullptr) + (w->s_out != nullptr) + (w->w2_8 != nullptr) + (w->s_2 != nullptr);
-  if (nf8b != 0 && (nf8b != 4 || nf8 != 4)) return false;
-  return true;
-}
-
-bool block_align_ok(const zi_block_weights* w) {
-  const void* ps[] = {w->w_qkv, w->w_out, w->w13, w->w2, w->g_attn1, w->g_attn2, w->g_ffn1, w->g_ffn2, w->g_q, w->g_k};
-  for (const void* p : ps)
-    if (!aligned16(p)) return false;
-  if (w->w_ada && !aligned16(w->w_ada)) return false;
-  if (w->w_qkv8 && (!aligned16(w->w_qkv8) || !aligned16(w->s_qkv) || !aligned16(w->w13_8) || !aligned16(w->s_13)))
-    return false;
-  if (w->w_out8 && (!aligned16(w->w_out8) || !aligned16(w->s_out) || !aligned16(w->w2_8) || !aligned16(w->s_2)))
-    return false;
-  return true;
-}
-
-// How the gated residual after the FFN hands over to the next norm.
-struct NextNormSpec {
-  int kind;            // NEXT_NONE / NEXT_RMS / NEXT_LAYERNORM
-  const uint16_t* gain;
-  const float* scale;  // [B][mod_ld] or null
-  int next_rows;       // h written for local rows < next_rows
-  bool f8 = false;     // the next block takes e4m3 h (NEXT_RMS only)
-};
-
-// A block runs its QKV and FFN w1|w3 projections in e4m3 when it carries e4m3 weights
-// for them, and also its output projection and FFN w2 when it carries those too.
-inline bool block_f8(const zi_block_weights* w) { return w && w->w_qkv8 != nullptr; }
-inline bool block_f8_all(const zi_block_weights* w) { return block_f8(w) && w->w_out8 != nullptr; }
-
-// One block over `rows` rows of the token buffer starting at global row `row_off`.
-// Pointers are local (row 0 = global row row_off).  h must already hold the
-// block's pre-attention norm output.
-struct BlockCtx {
-  DevInfo* dev;
-  const zi_config* cfg;
-  const zi_block_weights* w;
-  int rows, row_off, batch;
-  RowMap map;
-  float* x_in;
-  float* x_out;
-  uint16_t *h, *qkv, *att, *o, *u;
-  uint8_t* hq;  // the same buffer as h, as e4m3 codes (D bytes per row) for e4m3 blocks
-  float* hs;    // per-row scales of hq
-  uint8_t* q8;  // e4m3 codes of att or u (all-e4m3 blocks), and ...
-  float* q8s;   // ... their per-row scales
-  const float2* rope;  // pair-major [head_dim / 2][rope_n]
-  int rope_n;
-  const float* mod;  // this block's 4D modulation inside the per-batch vector, or null
-  int mod_ld;
-  int nseg;
-  int seg_row0[2], seg_len[2];  // local rows
-  const int* kv_len;  // [batch] keys of the last segment (valid text tokens), or null = all
-  SplitScratch split;  // split-tail scratch of the workspace (counters cleared)
-};
-
-int run_block(const BlockCtx& b, const NextNormSpec& next, cudaStream_t st) {
-  const int D = b.cfg->dim;
-  const int Fp = zi_ffn_padded(b.cfg->ffn);
-  const float eps = b.cfg->norm_eps;
-  // QKV projection with QK-RMSNorm + RoPE epilogue
-  EpiParams eq = epi_plain(b.qkv, 3 * D);
-  eq.rope = b.rope;
-  eq.rope_n = b.rope_n;
-  eq.g_q = b.w->g_q;
-  eq.g_k = b.w->g_k;
-  eq.eps = eps;
-  eq.dim = D;
-  eq.row_off = b.row_off;
-  eq.map = b.map;
-  const bool f8 = block_f8(b.w);
-  if (f8) {
-    eq.a_scale = b.hs;
-    eq.b_scale = b.w->s_qkv;
-    ZI_TRY((run_block_gemm<EPI_QKV, true>(b.dev, BIT_GEMM_QKV, ZI_KERNEL_GEMM_QKV, b.hq, b.w->w_qkv8, b.rows, 3 * D,
-                                          D, eq, st, b.split)));
-  } else {
-    ZI_TRY((run_block_gemm<EPI_QKV>(b.dev, BIT_GEMM_QKV, ZI_KERNEL_GEMM_QKV, b.h, b.w->w_qkv, b.rows, 3 * D, D, eq,
-                                    st, b.split)));
-  }
-  ZI_TRY(run_attention(b.dev, b.qkv, b.rows, b.att, D, b.cfg->heads, b.batch, b.nseg, b.seg_row0, b.seg_len,
-                       b.kv_len, st, b.split));
-  const bool f8all = block_f8_all(b.w);
-  if (f8all) {
-    ZI_TRY(run_quantize(b.att, b.rows, D, b.q8, b.q8s, st));
-    EpiParams eo = epi_plain(b.o, D);
-    eo.a_scale = b.q8s;
-    eo.b_scale = b.w->s_out;
-    ZI_TRY((run_block_gemm<EPI_BF16, true>(b.dev, BIT_GEMM_BF16, ZI_KERNEL_GEMM_OUT, b.q8, b.w->w_out8, b.rows, D,
-                                           D, eo, st, b.split)));
-  } else {
-    ZI_TRY((run_block_gemm<EPI_BF16>(b.dev, BIT_GEMM_BF16, ZI_KERNEL_GEMM_OUT, b.att, b.w->w_out, b.rows, D, D,
-                                     epi_plain(b.o, D), st, b.split)));
-  }
-  PostParams pa;
-  memset(&pa, 0, sizeof(pa));
-  pa.x_in = b.x_in;
-  pa.x_out = b.x_out;
-  pa.o = b.o;
-  pa.g_post = b.w->g_attn2;
-  pa.gate = b.mod ? b.mod + D : nullptr;
-  pa.gate_ld = b.mod_ld;
-  pa.next = NEXT_RMS;
-  pa.g_next = b.w->g_ffn1;
-  pa.scale = b.mod ? b.mod + 2 * D : nullptr;
-  pa.scale_ld = b.mod_ld;
-  pa.next_rows = b.rows;
-  pa.h = b.h;
-  pa.hq = f8 ? b.hq : nullptr;
-  pa.hs = f8 ? b.hs : nullptr;
-  pa.map = b.map;
-  pa.row_off = b.row_off;
-  pa.D = D;
-  pa.eps = eps;
-  pa.eps_ln = b.cfg->final_eps;
-  ZI_TRY(run_post(pa, b.rows, st));
-  if (f8) {
-    EpiParams e13 = epi_plain(b.u, Fp);
-    e13.a_scale = b.hs;
-    e13.b_scale = b.w->s_13;
-    ZI_TRY((run_block_gemm<EPI_SWIGLU, true>(b.dev, BIT_GEMM_SWIGLU, ZI_KERNEL_GEMM_FFN_UP, b.hq, b.w->w13_8, b.rows,
-                                             2 * Fp, D, e13, st, b.split)));
-  } else {
-    ZI_TRY((run_block_gemm<EPI_SWIGLU>(b.dev, BIT_GEMM_SWIGLU, ZI_KERNEL_GEMM_FFN_UP, b.h, b.w->w13, b.rows, 2 * Fp,
-                                       D, epi_plain(b.u, Fp), st, b.split)));
-  }
-  if (f8all) {
-    ZI_TRY(run_quantize(b.u, b.rows, Fp, b.q8, b.q8s, st));
-    EpiParams ed = epi_plain(b.o, D);
-    ed.a_scale = b.q8s;
-    ed.b_scale = b.w->s_2;
-    ZI_TRY((run_block_gemm<EPI_BF16, true>(b.dev, BIT_GEMM_BF16, ZI_KERNEL_GEMM_FFN_DOWN, b.q8, b.w->w2_8, b.rows,
-                                           D, Fp, ed, st, b.split)));
-  } else {
-    ZI_TRY((run_block_gemm<EPI_BF16>(b.dev, BIT_GEMM_BF16, ZI_KERNEL_GEMM_FFN_DOWN, b.u, b.w->w2, b.rows, D, Fp,
-                                     epi_plain(b.o, D), st, b.split)));
-  }
-  PostParams pf = pa;
-  pf.x_in = b.x_out;
-  pf.g_post = b.w->g_ffn2;
-  pf.gate = b.mod ? b.mod + 3 * D : nullptr;
-  pf.next = next.kind;
-  pf.g_next = next.gain;
-  pf.scale = next.scale;
-  pf.next_rows = next.next_rows;
-  pf.hq = (next.kind == NEXT_RMS && next.f8) ? b.hq : nullptr;
-  pf.hs = (next.kind == NEXT_RMS && next.f8) ? b.hs : nullptr;
-  return run_post(pf, b.rows, st);
-}
-
-int run_ada(const AdaSegs& segs, const float* c, const float* silu_c, int batch, int out_ld, float* out,
-            cudaStream_t st) {
-  int max_rows = 0;
-  for (int i = 0; i < segs.n; ++i) max_rows = segs.rows[i] > max_rows ? segs.rows[i] : max_rows;
-  dim3 grid((max_rows + 63) / 64, segs.n);
-  prof_pre(st);
-  ada_gemv_kernel<<<grid, 256, 0, st>>>(segs, c, silu_c, batch, out_ld, out);
-  return launched(ZI_KERNEL_ADALN, st);
-}
-
-// pos_major: out [n][pairs] (the zi_rope_table layout); else [pairs][n] for the QKV epilogue.
-int run_rope(const zi_config& cfg, const int32_t* pos, int n, float2* out, cudaStream_t st, bool pos_major) {
-  const int pairs = cfg.head_dim / 2;
-  const int total = n * pairs;
-  prof_pre(st);
-  rope_table_kernel<<<(total + 255) / 256, 256, 0, st>>>(pos, n, cfg.rope_axes[0], cfg.rope_axes[1],
-                                                           cfg.rope_axes[2], double(cfg.rope_theta), out,
-                                                           pos_major ? 1 : 0);
-  return launched(ZI_KERNEL_ROPE, st);
-}
-
-// Elementwise 2^x through the attention softmax's FMA-pipe exponential (exp2_poly_pair),
-// for the test hook zi_exp2_poly.
-__global__ void exp2_poly_kernel(const float* __restrict__ x, float* __restrict__ y, size_t n) {
-  const size_t i = 2 * (size_t(blockIdx.x) * blockDim.x + threadIdx.x);
-  if (i >= n) return;
-  const bool two = i + 1 < n;
-  float e0, e1;
-  exp2_poly_pair(x[i], two ? x[i + 1] : 0.f, e0, e1);
-  y[i] = e0;
-  if (two) y[i + 1] = e1;
-}
-
 // ---------------------------------------------------------------- clusters
 
 // Raise a kernel's dynamic shared-memory limit once per device (kernels outside KernelBit).
@@ -731,8 +443,9 @@ int make_scale_map(CUtensorMap* m, const uint8_t* base, int tiles_x, int tiles_y
   return r == CUDA_SUCCESS ? ZI_OK : ZI_ERR_CUDA;
 }
 
-template <int FMT>
-int run_fp4_wide(DevInfo* dev, const uint8_t* a, const uint8_t* b, const fp4::GemmParams& p, cudaStream_t st) {
+template <int FMT, int EPI>
+int run_fp4_wide(DevInfo* dev, int kind, const uint8_t* a, const uint8_t* b, const fp4::GemmParams& p,
+                 const EpiParams& ep, cudaStream_t st) {
   using L = fp4::WideSmem<FMT>;
   if (dev->sms < 2) return ZI_ERR_DEVICE;
   CUtensorMap ta, tb, tsa, tsb;
@@ -741,7 +454,7 @@ int run_fp4_wide(DevInfo* dev, const uint8_t* a, const uint8_t* b, const fp4::Ge
   const int tx = fp4::tiles_along<FMT>(p.K);
   ZI_TRY(make_scale_map(&tsa, p.abs, tx, fp4::tiles_down(p.M), fp4::kStageTiles<FMT>));
   ZI_TRY(make_scale_map(&tsb, p.bbs, tx, fp4::tiles_down(p.N), fp4::kStageTiles<FMT>));
-  constexpr auto kern = fp4::gemm_wide_kernel<FMT>;
+  constexpr auto kern = fp4::gemm_wide_kernel<FMT, EPI>;
   ZI_TRY((raise_smem<kern>(dev, int(L::kBytes))));
   const int num_m = (p.M + 255) / 256, num_n = (p.N + 255) / 256;
   const long long tiles = static_cast<long long>(num_m) * num_n;
@@ -752,8 +465,8 @@ int run_fp4_wide(DevInfo* dev, const uint8_t* a, const uint8_t* b, const fp4::Ge
   const TailSched sched = make_tail_sched(int(tiles), dev->sms / 2, (p.K + fp4::kStageK - 1) / fp4::kStageK, false, num_n,
                                           group, group_n);
   prof_pre(st);
-  kern<<<2 * sched_units(sched, int(tiles)), fp4::kWideThreads, L::kBytes, st>>>(ta, tb, tsa, tsb, p, sched);
-  return launched(ZI_KERNEL_GEMM_FP4, st);
+  kern<<<2 * sched_units(sched, int(tiles)), fp4::kWideThreads, L::kBytes, st>>>(ta, tb, tsa, tsb, p, ep, sched);
+  return launched(kind, st);
 }
 
 // Up to 64 rows of A the narrow kernel's tiles fit the rows; past that it is taken while its 128 x 128 tiles are
@@ -767,7 +480,349 @@ int run_fp4_gemm(DevInfo* dev, const uint8_t* a, const uint8_t* b, const fp4::Ge
   if (p.M <= 64) return run_fp4_narrow<FMT, 64>(dev, a, b, p, st);
   const long long tiles = static_cast<long long>((p.M + 127) / 128) * ((p.N + 127) / 128);
   if (8 * tiles <= 9LL * dev->sms) return run_fp4_narrow<FMT, 128>(dev, a, b, p, st);
-  return run_fp4_wide<FMT>(dev, a, b, p, st);
+  return run_fp4_wide<FMT, EPI_BF16>(dev, ZI_KERNEL_GEMM_FP4, a, b, p, epi_plain(p.out, p.N), st);
+}
+
+// ---------------------------------------------------------------- row kernels
+
+// hq non-null: the output is e4m3 codes [rows][D] with per-row scales hs instead of bf16 h.
+template <typename TIn>
+int run_rms_mod(const TIn* x, int rows, int D, const uint16_t* gain, const float* scale, int scale_ld, RowMap map,
+                int row_off, float eps, uint16_t* h, cudaStream_t st, uint8_t* hq = nullptr, float* hs = nullptr) {
+  if (rows <= 0) return ZI_OK;
+  prof_pre(st);
+  rms_mod_kernel<TIn><<<rows, kRowThreads, 0, st>>>(x, D, gain, scale, scale_ld, map, row_off, eps, h, hq, hs);
+  return launched(ZI_KERNEL_PRE_NORM, st);
+}
+
+// Per-row e4m3 codes and scales of a [rows, cols] fp32 or bf16 matrix (cols <= 16384).
+constexpr int kQuantMaxCols = kRowThreads * 16 * 4;
+template <typename TIn>
+int run_quantize(const TIn* x, int rows, int cols, uint8_t* q, float* sc, cudaStream_t st) {
+  if (rows <= 0) return ZI_OK;
+  prof_pre(st);
+  if (cols <= kRowThreads * kRowMaxVec * 4)
+    quantize_rows_e4m3_kernel<TIn, kRowMaxVec><<<rows, kRowThreads, 0, st>>>(x, cols, q, sc);
+  else
+    quantize_rows_e4m3_kernel<TIn, 16><<<rows, kRowThreads, 0, st>>>(x, cols, q, sc);
+  return launched(ZI_KERNEL_QUANTIZE, st);
+}
+
+int run_post(const PostParams& p, int rows, cudaStream_t st) {
+  if (rows <= 0) return ZI_OK;
+  prof_pre(st);
+  post_residual_kernel<<<rows, kRowThreads, 0, st>>>(p);
+  return launched(ZI_KERNEL_POST_NORM, st);
+}
+
+// ---------------------------------------------------------------- workspace
+
+constexpr size_t kAlign = 1024;
+inline size_t up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
+
+// Bytes of one activation matrix in 4 bits: codes, block scales, row scales.
+inline size_t fp4_act_bytes(size_t rows, size_t cols) {
+  return rows * (cols / 2) + size_t(fp4::tiles_down(int(rows))) * fp4::tiles_along<fp4::NV>(int(cols)) * fp4::kTileBytes +
+         rows * 4 + 64;
+}
+
+struct Ws {
+  size_t mod, c, silu, hid, lens, pos, rope, x, h, hs, qkv, att, o, u, q8, q8s, tok, capn, split_cnt, split_part,
+      total;
+};
+
+Ws carve(const zi_config& cfg, int batch, int s_img, int s_txt, bool model, int mod_cols) {
+  const size_t D = size_t(cfg.dim);
+  const size_t S = size_t(s_img) + size_t(s_txt);
+  const size_t rows = size_t(batch) * S;
+  const size_t Fp = size_t(zi_ffn_padded(cfg.ffn));
+  const size_t pairs = size_t(cfg.head_dim) / 2;
+  Ws w;
+  size_t o = 0;
+  w.mod = o; o = up(o + size_t(batch) * size_t(mod_cols) * 4);
+  w.c = o; o = up(o + (model ? size_t(batch) * 256 * 4 : 0));
+  w.silu = o; o = up(o + (model ? size_t(batch) * 256 * 4 : 0));
+  w.hid = o; o = up(o + (model ? size_t(batch) * size_t(cfg.t_mid) * 4 : 0));
+  // a model forward may give every batch element its own positions (text lengths)
+  const size_t tab_rows = model ? rows : S;
+  w.lens = o; o = up(o + (model ? size_t(batch) * 4 : 0));
+  w.pos = o; o = up(o + (model ? tab_rows * 3 * 4 : 0));
+  w.rope = o; o = up(o + tab_rows * pairs * 8);
+  w.x = o; o = up(o + (model ? rows * D * 4 : 0));
+  w.h = o; o = up(o + rows * D * 2);  // bf16 h, or e4m3 codes (rows x D bytes) for e4m3 blocks
+  w.hs = o; o = up(o + rows * 4);      // per-row scales of e4m3 h
+  w.qkv = o; o = up(o + rows * 3 * D * 2);
+  w.att = o; o = up(o + rows * D * 2);
+  w.o = o; o = up(o + rows * D * 2);
+  w.u = o; o = up(o + rows * Fp * 2);
+  // e4m3 codes of the attention output or of u (never live together) and their row scales
+  // ... or, for 4-bit blocks, h, the attention output or u in 4 bits
+  const size_t wide = Fp > D ? Fp : D, f4 = fp4_act_bytes(rows, wide);
+  w.q8 = o; o = up(o + (rows * wide > f4 ? rows * wide : f4));
+  w.q8s = o; o = up(o + rows * 4);
+  w.tok = o; o = up(o + (model ? size_t(batch) * s_img * size_t(4 * cfg.in_ch) * 2 : 0));
+  w.capn = o; o = up(o + (model ? size_t(batch) * s_txt * size_t(cfg.cap_dim) * 2 : 0));
+  w.split_cnt = o; o = up(o + size_t(kSplitSlots) * 4);
+  w.split_part = o; o = up(o + size_t(kSplitSlots) * kSplitSlotBytes);
+  w.total = o;
+  return w;
+}
+
+int check_cfg(const zi_config* c) {
+  if (!c) return ZI_ERR_ARG;
+  if (c->head_dim != 128 || c->patch != 2) return ZI_ERR_SHAPE;
+  if (c->dim <= 0 || c->dim % 256 != 0 || c->dim != c->heads * c->head_dim || c->dim > 4096) return ZI_ERR_SHAPE;
+  if (c->rope_axes[0] + c->rope_axes[1] + c->rope_axes[2] != c->head_dim) return ZI_ERR_SHAPE;
+  for (int i = 0; i < 3; ++i)
+    if (c->rope_axes[i] <= 0 || c->rope_axes[i] % 2) return ZI_ERR_SHAPE;
+  if (c->ffn <= 0 || c->cap_dim <= 0 || c->cap_dim % 64 != 0 || c->cap_dim > 4096) return ZI_ERR_SHAPE;
+  if (c->t_freq != 256 || c->t_mid <= 0 || c->t_mid % 8) return ZI_ERR_SHAPE;  // warp-per-row timestep MLP
+  if ((c->dim < 256 ? c->dim : 256) != 256) return ZI_ERR_SHAPE;  // adaLN GEMV is 256 wide
+  if (4 * c->in_ch != 64) return ZI_ERR_SHAPE;                     // final linear uses a 64-wide tile
+  if (c->n_noise < 0 || c->n_ctx < 0 || c->n_main < 1 || c->n_noise + c->n_main + 1 > kMaxAdaSegs)
+    return ZI_ERR_SHAPE;
+  return ZI_OK;
+}
+
+bool block_ptrs_ok(const zi_block_weights* w, bool need_mod) {
+  if (!w) return false;
+  const void* ps[] = {w->w_qkv, w->w_out, w->w13, w->w2, w->g_attn1, w->g_attn2, w->g_ffn1, w->g_ffn2, w->g_q, w->g_k};
+  for (const void* p : ps)
+    if (!p) return false;
+  if (need_mod && (!w->w_ada || !w->b_ada)) return false;
+  if ((w->w_ada == nullptr) != (w->b_ada == nullptr)) return false;
+  // e4m3 projections: all four of w_qkv8, s_qkv, w13_8, s_13, or none; then optionally
+  // all four of w_out8, s_out, w2_8, s_2
+  const int nf8 = (w->w_qkv8 != nullptr) + (w->s_qkv != nullptr) + (w->w13_8 != nullptr) + (w->s_13 != nullptr);
+  if (nf8 != 0 && nf8 != 4) return false;
+  const int nf8b = (w->w_out8 != nullptr) + (w->s_out != nullptr) + (w->w2_8 != nullptr) + (w->s_2 != nullptr);
+  if (nf8b != 0 && (nf8b != 4 || nf8 != 4)) return false;
+  // 4-bit projections: codes and block scales of QKV and w1|w3 (or none), then optionally of the output projection
+  // and w2; row scales for all of them (NVFP4) or for none (MXFP4); not beside e4m3 ones
+  const int n4 = (w->w_qkv4 != nullptr) + (w->b_qkv4 != nullptr) + (w->w13_4 != nullptr) + (w->b_13_4 != nullptr);
+  const int n4b = (w->w_out4 != nullptr) + (w->b_out4 != nullptr) + (w->w2_4 != nullptr) + (w->b_2_4 != nullptr);
+  if ((n4 != 0 && n4 != 4) || (n4b != 0 && (n4b != 4 || n4 != 4)) || (n4 != 0 && nf8 != 0)) return false;
+  const int r4 = (w->r_qkv4 != nullptr) + (w->r_13_4 != nullptr), r4b = (w->r_out4 != nullptr) + (w->r_2_4 != nullptr);
+  if (r4 + r4b != 0 && (n4 != 4 || r4 != 2 || r4b != (n4b ? 2 : 0))) return false;
+  return true;
+}
+
+bool block_align_ok(const zi_block_weights* w) {
+  const void* ps[] = {w->w_qkv, w->w_out, w->w13, w->w2, w->g_attn1, w->g_attn2, w->g_ffn1, w->g_ffn2, w->g_q, w->g_k};
+  for (const void* p : ps)
+    if (!aligned16(p)) return false;
+  if (w->w_ada && !aligned16(w->w_ada)) return false;
+  if (w->w_qkv8 && (!aligned16(w->w_qkv8) || !aligned16(w->s_qkv) || !aligned16(w->w13_8) || !aligned16(w->s_13)))
+    return false;
+  if (w->w_out8 && (!aligned16(w->w_out8) || !aligned16(w->s_out) || !aligned16(w->w2_8) || !aligned16(w->s_2)))
+    return false;
+  const void* p4[] = {w->w_qkv4, w->b_qkv4, w->r_qkv4, w->w13_4, w->b_13_4, w->r_13_4,
+                      w->w_out4, w->b_out4, w->r_out4, w->w2_4,  w->b_2_4,  w->r_2_4};
+  for (const void* p : p4)
+    if (!aligned16(p)) return false;
+  return true;
+}
+
+// How the gated residual after the FFN hands over to the next norm.
+struct NextNormSpec {
+  int kind;            // NEXT_NONE / NEXT_RMS / NEXT_LAYERNORM
+  const uint16_t* gain;
+  const float* scale;  // [B][mod_ld] or null
+  int next_rows;       // h written for local rows < next_rows
+  bool f8 = false;     // the next block takes e4m3 h (NEXT_RMS only)
+};
+
+// A block runs its QKV and FFN w1|w3 projections in e4m3 when it carries e4m3 weights
+// for them, and also its output projection and FFN w2 when it carries those too.
+inline bool block_f8(const zi_block_weights* w) { return w && w->w_qkv8 != nullptr; }
+inline bool block_f8_all(const zi_block_weights* w) { return block_f8(w) && w->w_out8 != nullptr; }
+
+// ... or in 4 bits, likewise.  A block in 4 bits takes bf16 h as a bf16 block does, so both may stand in one model.
+inline bool block_f4(const zi_block_weights* w) { return w && w->w_qkv4 != nullptr; }
+inline bool block_f4_all(const zi_block_weights* w) { return block_f4(w) && w->w_out4 != nullptr; }
+
+// One projection of a block in 4 bits: the rows of x [rows, K] (bf16) to `buf`, then the product with W [N, K].
+template <int EPI>
+int run_fp4_projection(DevInfo* dev, int kind, const uint16_t* x, int rows, int K, const uint8_t* w, const uint8_t* wbs,
+                       const float* wrs, int N, uint8_t* buf, const EpiParams& ep, cudaStream_t st) {
+  if (rows <= 0) return ZI_OK;
+  uint8_t* q = buf;
+  uint8_t* bs = buf + (size_t(rows) * (K / 2) + 15) / 16 * 16;
+  const size_t tiles = size_t(fp4::tiles_down(rows)) * (wrs ? fp4::tiles_along<fp4::NV>(K) : fp4::tiles_along<fp4::MX>(K));
+  float* rs = reinterpret_cast<float*>(bs + tiles * fp4::kTileBytes);
+  const fp4::GemmParams p{bs, wbs, wrs ? rs : nullptr, wrs, static_cast<uint16_t*>(ep.out), rows, N, K};
+  if (wrs) {
+    ZI_TRY((run_quantize_fp4<fp4::NV>(x, rows, K, q, bs, rs, st)));
+    return run_fp4_wide<fp4::NV, EPI>(dev, kind, q, w, p, ep, st);
+  }
+  ZI_TRY((run_quantize_fp4<fp4::MX>(x, rows, K, q, bs, static_cast<float*>(nullptr), st)));
+  return run_fp4_wide<fp4::MX, EPI>(dev, kind, q, w, p, ep, st);
+}
+
+// One block over `rows` rows of the token buffer starting at global row `row_off`.
+// Pointers are local (row 0 = global row row_off).  h must already hold the
+// block's pre-attention norm output.
+struct BlockCtx {
+  DevInfo* dev;
+  const zi_config* cfg;
+  const zi_block_weights* w;
+  int rows, row_off, batch;
+  RowMap map;
+  float* x_in;
+  float* x_out;
+  uint16_t *h, *qkv, *att, *o, *u;
+  uint8_t* hq;  // the same buffer as h, as e4m3 codes (D bytes per row) for e4m3 blocks
+  float* hs;    // per-row scales of hq
+  uint8_t* q8;  // e4m3 codes of att or u (all-e4m3 blocks), and ...
+  float* q8s;   // ... their per-row scales
+  uint8_t* q4;  // one activation matrix in 4 bits (4-bit blocks; fp4_act_bytes of all rows)
+  const float2* rope;  // pair-major [head_dim / 2][rope_n]
+  int rope_n;
+  const float* mod;  // this block's 4D modulation inside the per-batch vector, or null
+  int mod_ld;
+  int nseg;
+  int seg_row0[2], seg_len[2];  // local rows
+  const int* kv_len;  // [batch] keys of the last segment (valid text tokens), or null = all
+  SplitScratch split;  // split-tail scratch of the workspace (counters cleared)
+};
+
+int run_block(const BlockCtx& b, const NextNormSpec& next, cudaStream_t st) {
+  const int D = b.cfg->dim;
+  const int Fp = zi_ffn_padded(b.cfg->ffn);
+  const float eps = b.cfg->norm_eps;
+  // QKV projection with QK-RMSNorm + RoPE epilogue
+  EpiParams eq = epi_plain(b.qkv, 3 * D);
+  eq.rope = b.rope;
+  eq.rope_n = b.rope_n;
+  eq.g_q = b.w->g_q;
+  eq.g_k = b.w->g_k;
+  eq.eps = eps;
+  eq.dim = D;
+  eq.row_off = b.row_off;
+  eq.map = b.map;
+  const bool f8 = block_f8(b.w), f4 = block_f4(b.w), f4all = block_f4_all(b.w);
+  if (f4) {
+    ZI_TRY((run_fp4_projection<EPI_QKV>(b.dev, ZI_KERNEL_GEMM_QKV, b.h, b.rows, D, b.w->w_qkv4, b.w->b_qkv4, b.w->r_qkv4,
+                                        3 * D, b.q4, eq, st)));
+  } else if (f8) {
+    eq.a_scale = b.hs;
+    eq.b_scale = b.w->s_qkv;
+    ZI_TRY((run_block_gemm<EPI_QKV, true>(b.dev, BIT_GEMM_QKV, ZI_KERNEL_GEMM_QKV, b.hq, b.w->w_qkv8, b.rows, 3 * D,
+                                          D, eq, st, b.split)));
+  } else {
+    ZI_TRY((run_block_gemm<EPI_QKV>(b.dev, BIT_GEMM_QKV, ZI_KERNEL_GEMM_QKV, b.h, b.w->w_qkv, b.rows, 3 * D, D, eq,
+                                    st, b.split)));
+  }
+  ZI_TRY(run_attention(b.dev, b.qkv, b.rows, b.att, D, b.cfg->heads, b.batch, b.nseg, b.seg_row0, b.seg_len,
+                       b.kv_len, st, b.split));
+  const bool f8all = block_f8_all(b.w);
+  if (f4all) {
+    ZI_TRY((run_fp4_projection<EPI_BF16>(b.dev, ZI_KERNEL_GEMM_OUT, b.att, b.rows, D, b.w->w_out4, b.w->b_out4, b.w->r_out4,
+                                         D, b.q4, epi_plain(b.o, D), st)));
+  } else if (f8all) {
+    ZI_TRY(run_quantize(b.att, b.rows, D, b.q8, b.q8s, st));
+    EpiParams eo = epi_plain(b.o, D);
+    eo.a_scale = b.q8s;
+    eo.b_scale = b.w->s_out;
+    ZI_TRY((run_block_gemm<EPI_BF16, true>(b.dev, BIT_GEMM_BF16, ZI_KERNEL_GEMM_OUT, b.q8, b.w->w_out8, b.rows, D,
+                                           D, eo, st, b.split)));
+  } else {
+    ZI_TRY((run_block_gemm<EPI_BF16>(b.dev, BIT_GEMM_BF16, ZI_KERNEL_GEMM_OUT, b.att, b.w->w_out, b.rows, D, D,
+                                     epi_plain(b.o, D), st, b.split)));
+  }
+  PostParams pa;
+  memset(&pa, 0, sizeof(pa));
+  pa.x_in = b.x_in;
+  pa.x_out = b.x_out;
+  pa.o = b.o;
+  pa.g_post = b.w->g_attn2;
+  pa.gate = b.mod ? b.mod + D : nullptr;
+  pa.gate_ld = b.mod_ld;
+  pa.next = NEXT_RMS;
+  pa.g_next = b.w->g_ffn1;
+  pa.scale = b.mod ? b.mod + 2 * D : nullptr;
+  pa.scale_ld = b.mod_ld;
+  pa.next_rows = b.rows;
+  pa.h = b.h;
+  pa.hq = f8 ? b.hq : nullptr;
+  pa.hs = f8 ? b.hs : nullptr;
+  pa.map = b.map;
+  pa.row_off = b.row_off;
+  pa.D = D;
+  pa.eps = eps;
+  pa.eps_ln = b.cfg->final_eps;
+  ZI_TRY(run_post(pa, b.rows, st));
+  if (f4) {
+    ZI_TRY((run_fp4_projection<EPI_SWIGLU>(b.dev, ZI_KERNEL_GEMM_FFN_UP, b.h, b.rows, D, b.w->w13_4, b.w->b_13_4,
+                                           b.w->r_13_4, 2 * Fp, b.q4, epi_plain(b.u, Fp), st)));
+  } else if (f8) {
+    EpiParams e13 = epi_plain(b.u, Fp);
+    e13.a_scale = b.hs;
+    e13.b_scale = b.w->s_13;
+    ZI_TRY((run_block_gemm<EPI_SWIGLU, true>(b.dev, BIT_GEMM_SWIGLU, ZI_KERNEL_GEMM_FFN_UP, b.hq, b.w->w13_8, b.rows,
+                                             2 * Fp, D, e13, st, b.split)));
+  } else {
+    ZI_TRY((run_block_gemm<EPI_SWIGLU>(b.dev, BIT_GEMM_SWIGLU, ZI_KERNEL_GEMM_FFN_UP, b.h, b.w->w13, b.rows, 2 * Fp,
+                                       D, epi_plain(b.u, Fp), st, b.split)));
+  }
+  if (f4all) {
+    ZI_TRY((run_fp4_projection<EPI_BF16>(b.dev, ZI_KERNEL_GEMM_FFN_DOWN, b.u, b.rows, Fp, b.w->w2_4, b.w->b_2_4, b.w->r_2_4,
+                                         D, b.q4, epi_plain(b.o, D), st)));
+  } else if (f8all) {
+    ZI_TRY(run_quantize(b.u, b.rows, Fp, b.q8, b.q8s, st));
+    EpiParams ed = epi_plain(b.o, D);
+    ed.a_scale = b.q8s;
+    ed.b_scale = b.w->s_2;
+    ZI_TRY((run_block_gemm<EPI_BF16, true>(b.dev, BIT_GEMM_BF16, ZI_KERNEL_GEMM_FFN_DOWN, b.q8, b.w->w2_8, b.rows,
+                                           D, Fp, ed, st, b.split)));
+  } else {
+    ZI_TRY((run_block_gemm<EPI_BF16>(b.dev, BIT_GEMM_BF16, ZI_KERNEL_GEMM_FFN_DOWN, b.u, b.w->w2, b.rows, D, Fp,
+                                     epi_plain(b.o, D), st, b.split)));
+  }
+  PostParams pf = pa;
+  pf.x_in = b.x_out;
+  pf.g_post = b.w->g_ffn2;
+  pf.gate = b.mod ? b.mod + 3 * D : nullptr;
+  pf.next = next.kind;
+  pf.g_next = next.gain;
+  pf.scale = next.scale;
+  pf.next_rows = next.next_rows;
+  pf.hq = (next.kind == NEXT_RMS && next.f8) ? b.hq : nullptr;
+  pf.hs = (next.kind == NEXT_RMS && next.f8) ? b.hs : nullptr;
+  return run_post(pf, b.rows, st);
+}
+
+int run_ada(const AdaSegs& segs, const float* c, const float* silu_c, int batch, int out_ld, float* out,
+            cudaStream_t st) {
+  int max_rows = 0;
+  for (int i = 0; i < segs.n; ++i) max_rows = segs.rows[i] > max_rows ? segs.rows[i] : max_rows;
+  dim3 grid((max_rows + 63) / 64, segs.n);
+  prof_pre(st);
+  ada_gemv_kernel<<<grid, 256, 0, st>>>(segs, c, silu_c, batch, out_ld, out);
+  return launched(ZI_KERNEL_ADALN, st);
+}
+
+// pos_major: out [n][pairs] (the zi_rope_table layout); else [pairs][n] for the QKV epilogue.
+int run_rope(const zi_config& cfg, const int32_t* pos, int n, float2* out, cudaStream_t st, bool pos_major) {
+  const int pairs = cfg.head_dim / 2;
+  const int total = n * pairs;
+  prof_pre(st);
+  rope_table_kernel<<<(total + 255) / 256, 256, 0, st>>>(pos, n, cfg.rope_axes[0], cfg.rope_axes[1],
+                                                           cfg.rope_axes[2], double(cfg.rope_theta), out,
+                                                           pos_major ? 1 : 0);
+  return launched(ZI_KERNEL_ROPE, st);
+}
+
+// Elementwise 2^x through the attention softmax's FMA-pipe exponential (exp2_poly_pair),
+// for the test hook zi_exp2_poly.
+__global__ void exp2_poly_kernel(const float* __restrict__ x, float* __restrict__ y, size_t n) {
+  const size_t i = 2 * (size_t(blockIdx.x) * blockDim.x + threadIdx.x);
+  if (i >= n) return;
+  const bool two = i + 1 < n;
+  float e0, e1;
+  exp2_poly_pair(x[i], two ? x[i + 1] : 0.f, e0, e1);
+  y[i] = e0;
+  if (two) y[i + 1] = e1;
 }
 
 // ---------------------------------------------------------------- masked attention
@@ -1257,6 +1312,7 @@ int zi_block_forward(const zi_config* cfg, const zi_block_weights* w, const floa
   if (!block_align_ok(w) || !aligned16(d_x_in) || !aligned16(d_x_out) || (d_c && !aligned16(d_c)))
     return ZI_ERR_ALIGN;
   if (size_t(batch) * seq > (size_t(1) << 30) || batch > 65535) return ZI_ERR_SHAPE;
+  if (block_f4_all(w) && zi_ffn_padded(cfg->ffn) > kFp4MaxCols) return ZI_ERR_SHAPE;
   const Ws L = carve(*cfg, batch, seq, 0, false, 4 * cfg->dim);
   if (!d_ws || ws_bytes < L.total) return ZI_ERR_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(d_ws) & 255u) return ZI_ERR_ALIGN;
@@ -1295,7 +1351,7 @@ int zi_block_forward(const zi_config* cfg, const zi_block_weights* w, const floa
   b.h = reinterpret_cast<uint16_t*>(ws + L.h);
   b.hq = ws + L.h;
   b.hs = reinterpret_cast<float*>(ws + L.hs);
-  b.q8 = ws + L.q8;
+  b.q8 = b.q4 = ws + L.q8;
   b.q8s = reinterpret_cast<float*>(ws + L.q8s);
   b.qkv = reinterpret_cast<uint16_t*>(ws + L.qkv);
   b.att = reinterpret_cast<uint16_t*>(ws + L.att);
@@ -1376,6 +1432,14 @@ int model_forward_impl(const zi_config* cfg, const zi_model_weights* w, int batc
     if (block_f8_all(&w->ctx[i]) != f8all) return ZI_ERR_ARG;
   for (int i = 0; i < cfg->n_main; ++i)
     if (block_f8_all(&w->main[i]) != f8all) return ZI_ERR_ARG;
+  if (zi_ffn_padded(cfg->ffn) > kFp4MaxCols) {
+    for (int i = 0; i < cfg->n_noise; ++i)
+      if (block_f4_all(&w->noise[i])) return ZI_ERR_SHAPE;
+    for (int i = 0; i < cfg->n_ctx; ++i)
+      if (block_f4_all(&w->ctx[i])) return ZI_ERR_SHAPE;
+    for (int i = 0; i < cfg->n_main; ++i)
+      if (block_f4_all(&w->main[i])) return ZI_ERR_SHAPE;
+  }
   if (!aligned16(w->x_emb_w) || !aligned16(w->cap_w) || !aligned16(w->final_w) || !aligned16(w->final_ada_w) ||
       !aligned16(w->x_emb_b) || !aligned16(w->cap_b) || !aligned16(w->cap_norm) || !aligned16(d_txt) ||
       !aligned16(d_latent) || !aligned16(d_out))
@@ -1529,6 +1593,7 @@ int model_forward_impl(const zi_config* cfg, const zi_model_weights* w, int batc
     b.hq = ws + L.h + size_t(row_off) * D;  // e4m3 rows are D bytes
     b.hs = hs + row_off;
     b.q8 = ws + L.q8 + size_t(row_off) * (Fp_ > D ? Fp_ : D);
+    b.q4 = ws + L.q8;  // the segments' blocks run one after the other
     b.q8s = reinterpret_cast<float*>(ws + L.q8s) + row_off;
     b.qkv = qkv + size_t(row_off) * 3 * D;
     b.att = att + size_t(row_off) * D;

@@ -127,6 +127,24 @@ class DeviceBlock:
         b._finish(fp8)
         return b
 
+    def with_fp4(self, fmt: str = "nvfp4", projections=True) -> "DeviceBlock":
+        """The same block sharing these bf16 tensors, its projections in 4 bits made from them
+        (zi_quantize_fp4): projections=True QKV and FFN w1|w3, "all" the output projection and
+        FFN w2 too."""
+        if projections not in (True, "all"):
+            raise ValueError('projections: True or "all"')
+        b = DeviceBlock.__new__(DeviceBlock)
+        b.t = {k: v for k, v in self.t.items() if k in self.BF16_FIELDS}
+        b.modulated = self.modulated
+        for src, names in (("w_qkv", ("w_qkv4", "b_qkv4", "r_qkv4")), ("w13", ("w13_4", "b_13_4", "r_13_4")),
+                           ("w_out", ("w_out4", "b_out4", "r_out4")), ("w2", ("w2_4", "b_2_4", "r_2_4"))):
+            if projections == "all" or src in ("w_qkv", "w13"):
+                m = quantize_fp4(b.t[src], fmt)
+                parts = (m.codes, m.block_scales, m.row_scales)
+                b.t.update({n: t for n, t in zip(names, parts) if t is not None})
+        b._finish(False)
+        return b
+
     def nbytes(self) -> int:
         return sum(t.numel() * t.element_size() for t in self.t.values())
 
@@ -175,6 +193,17 @@ class DiT:
         other.noise = [b.with_e4m3(fp8) for b in self.noise]
         other.ctx = [b.with_e4m3(fp8) for b in self.ctx]
         other.main = [b.with_e4m3(fp8) for b in self.main]
+        other._bind()
+        return other
+
+    def with_fp4(self, fmt: str = "nvfp4", projections=True) -> "DiT":
+        """This transformer with its block projections in 4 bits (see DeviceBlock.with_fp4), sharing
+        the resident bf16 weights: only the 4-bit codes and their scales are new."""
+        other = DiT.__new__(DiT)
+        other.cfg, other.device, other.top, other.fp8 = self.cfg, self.device, self.top, False
+        other.noise = [b.with_fp4(fmt, projections) for b in self.noise]
+        other.ctx = [b.with_fp4(fmt, projections) for b in self.ctx]
+        other.main = [b.with_fp4(fmt, projections) for b in self.main]
         other._bind()
         return other
 
