@@ -138,11 +138,16 @@ ZI_DEV float off_border(float q, float a, float b) {
   return q;
 }
 
-// e4m3 byte of an NVFP4 block: amax / (6 r), rounded to nearest even.
+// e4m3 byte of an NVFP4 block: amax / (6 r), rounded to nearest even.  A bf16 amax (8 bits) over 6
+// is a border between two e4m3 values exactly or at least 2^-8 of its value away from it, so
+// rounding the approximate quotient to fp16 first (11 bits) lands on the border if and only
+// if the exact quotient does.  For an fp32 amax the remainder decides.
+template <bool EXACT24>
 ZI_DEV uint32_t nv_scale(uint32_t amax, uint32_t row_exp) {
   if (amax >= kInfBits) return 0x7Fu;
   const float t = __uint_as_float(amax) * exp_float(254u - row_exp);  // amax / r, exact
   const float q0 = t * (1.f / 6.f);
+  if (!EXACT24) return __nv_cvt_halfraw_to_fp8(__half_raw(__float2half_rn(q0)), __NV_SATFINITE, __NV_E4M3);
   const float q = off_border(fmaf(fmaf(-q0, 6.f, t), 1.f / 6.f, q0), t, 6.f);  // one Newton step on the residual
   return __nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
 }
@@ -156,15 +161,16 @@ ZI_DEV float e4m3_float(uint32_t byte) {
 ZI_DEV uint2 codes16(const float* v) {
   uint32_t w[2];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    w[h] = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t b = __nv_cvt_float2_to_fp4x2(make_float2(v[8 * h + 2 * i], v[8 * h + 2 * i + 1]), __NV_E2M1,
-                                                  cudaRoundNearest);
-      w[h] |= b << (8 * i);
-    }
-  }
+  for (int h = 0; h < 2; ++h)
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(w[h])
+        : "f"(v[8 * h]), "f"(v[8 * h + 1]), "f"(v[8 * h + 2]), "f"(v[8 * h + 3]), "f"(v[8 * h + 4]), "f"(v[8 * h + 5]),
+          "f"(v[8 * h + 6]), "f"(v[8 * h + 7]));
   return make_uint2(w[0], w[1]);
 }
 
@@ -245,14 +251,15 @@ __global__ void __launch_bounds__(kRowsThreads) quantize_kernel(const TIn* __res
       for (int e = 0; e < int(sizeof(TIn)); ++e) s[k].w[e] = make_uint4(0, 0, 0, 0);
     }
   }
+  uint32_t top[NB];  // the spans' largest |x|
+#pragma unroll
+  for (int k = 0; k < NB; ++k) top[k] = span_amax(s[k]);
   uint32_t row_exp = 127u;
   if constexpr (FMT == NV) {
     uint32_t am = 0;
 #pragma unroll
-    for (int k = 0; k < NB; ++k) {
-      const uint32_t a = span_amax(s[k]);
-      if (a < kInfBits) am = max(am, a);
-    }
+    for (int k = 0; k < NB; ++k)
+      if (top[k] < kInfBits) am = max(am, top[k]);
     for (int o = (tpr < 32 ? tpr : 32) >> 1; o > 0; o >>= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
     if (tpr > 32) {  // the row spans warps
       if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = am;
@@ -267,7 +274,7 @@ __global__ void __launch_bounds__(kRowsThreads) quantize_kernel(const TIn* __res
   for (int k = 0; k < NB; ++k) {
     const int i = sub + k * tpr;
     const bool have = row < rows && i < spans;
-    uint32_t amax = span_amax(s[k]);
+    uint32_t amax = top[k];
     if (FMT == MX) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     uint32_t byte = 0;
     if (have) {
@@ -280,7 +287,7 @@ __global__ void __launch_bounds__(kRowsThreads) quantize_kernel(const TIn* __res
         for (int e = 0; e < 16; e += 2)  // exact (a power of two), or far below half a step
           f2_unpack(f2_mul(f2_pack(v[e], v[e + 1]), inv2), v[e], v[e + 1]);
       } else {
-        byte = nv_scale(amax, row_exp);
+        byte = nv_scale<sizeof(TIn) == 4>(amax, row_exp);
         if (byte != 0u && byte != 0x7Fu) {
           nv_units<sizeof(TIn) == 4>(v, e4m3_float(byte), row_exp);
         } else {
