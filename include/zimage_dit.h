@@ -401,9 +401,9 @@ typedef struct zi_attention_desc {
   int kv_heads;
   int q_len;     /* queries per element, 1 .. 2^24 */
   int kv_len;    /* key rows per element, 1 .. 2^24 */
-  float scale;   /* of q . k; finite, > 0 (1 / sqrt(128) from zi_attention_desc_init) */
-  float softcap; /* scores become softcap * tanh(score / softcap); 0 = no cap; finite, >= 0 */
-  const float* d_slopes;       /* fp32 [heads] or NULL: scores lose slope[h] * |p_i - j|, after the cap */
+  float scale;   /* of q . k; 2^-60 .. 2^60 (1 / sqrt(128) from zi_attention_desc_init) */
+  float softcap; /* scores become softcap * tanh(score / softcap); 0 = no cap, else 2^-60 .. 2^60 */
+  const float* d_slopes;       /* fp32 [heads], finite, or NULL: scores lose slope[h] * |p_i - j|, after the cap */
   int causal;                  /* 1: query i sees key j only if j <= p_i (or by the prefix); 0: no order */
   const int32_t* d_prefix_len; /* int32 [batch] or NULL (needs causal): keys j < prefix[b] are seen by every query */
   const int32_t* d_kv_len;     /* int32 [batch] or NULL: keys of each element, clamped to [0, kv_len] on the device */

@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(few::kThreads)
         if (key >= n || id[e] < 0) used[e >> 1] &= (e & 1) ? 0x0000FFFFu : 0xFFFF0000u;
       }
     }
-    if (!mbar_wait(&full[slot], phase, abort_flag, ZI_DEVERR_TIMEOUT_SOFTMAX)) break;
+    if (!mbar_wait_warp(&full[slot], phase, abort_flag, ZI_DEVERR_TIMEOUT_SOFTMAX)) break;
     const uint32_t ks = smem_u32(ring + slot * kChunkBytes), vs = ks + 2 * kBox;
     float s[2][4];
 #pragma unroll
@@ -402,9 +402,11 @@ constexpr int kKSlots = 3, kVSlots = 2;
 constexpr uint32_t kQ0 = 0, kK0 = 2 * kTile, kV0 = kK0 + kKSlots * kTile;
 constexpr uint32_t kBar = kV0 + kVSlots * kTile;
 constexpr int kListTiles = 2048;  // key tiles whose state fits the lists; later ones are masked elementwise
-constexpr int kListWords = kListTiles / 16;  // of one row tile: 2 bits a key tile
-constexpr uint32_t kList = kBar + 256;
-constexpr uint32_t kSmemBytes = kList + 2 * kListWords * 4 + 1024;
+constexpr int kListWords = kListTiles / 32;
+constexpr uint32_t kList = kBar + 256;           // bit maps of the key tiles: seen [2 row tiles][kListWords], then full
+constexpr uint32_t kSmemBytes = kList + 4 * kListWords * 4 + 1024;
+constexpr uint32_t kScan = kK0;                  // ids of each key tile, before the rings are used: lowest, highest, any negative
+static_assert(kListTiles * 12 <= kBar - kK0, "the scan fits the rings");
 static_assert(kSmemBytes <= 232448, "shared memory");
 constexpr uint32_t kColS = 0, kColO = 256;
 // the partial of a split unit, over K and V: O [t][32 column quads][128 rows] float4, then (m, l) [256] float2
@@ -464,7 +466,8 @@ __global__ void __launch_bounds__(many::kThreads, 1)
   int* doc_min = lim_min + 4;  // of the rows' ids that are not negative ...
   int* doc_max = lim_min + 6;
   int* doc_neg = lim_min + 8;  // ... and whether any is
-  uint32_t* list = reinterpret_cast<uint32_t*>(smem + kList);  // [2][kListWords]
+  uint32_t* seen = reinterpret_cast<uint32_t*>(smem + kList);  // [2][kListWords] some row of the row tile sees some key ...
+  uint32_t* full = seen + 2 * kListWords;                      // ... every row every key
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // Blocks: rank fastest, then the key heads (of all batch elements) of a group, then the 256-row units from the
@@ -519,6 +522,47 @@ __global__ void __launch_bounds__(many::kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const bool skip = *abort_flag != 0;
 
+  const int* kd = p.k_doc ? p.k_doc + size_t(b) * p.kv_len : nullptr;
+  int* scan = reinterpret_cast<int*>(smem + kScan);
+  // Ranges of the document ids of key tiles first, first + step, ... below end; three tiles' loads on their way per warp
+  auto scan_ids = [&](int first, int step, int end) {
+    constexpr int kAhead = 3;
+    for (int j = first; j < end; j += step * kAhead) {
+      int d[kAhead][4];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int key = (j + u * step) * 128 + e * 32 + lane;
+          d[u][e] = key < n ? __ldg(kd + key) : -1;
+        }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        int lo = 0x7fffffff, hi = -1, neg = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (d[u][e] < 0) neg = 1;
+          else lo = min(lo, d[u][e]);
+          hi = max(hi, d[u][e]);
+        }
+        lo = __reduce_min_sync(0xffffffffu, lo);
+        hi = __reduce_max_sync(0xffffffffu, hi);
+        neg = __reduce_max_sync(0xffffffffu, neg);
+        const int jj = j + u * step;
+        if (lane == 0 && jj < end) {
+          scan[jj] = lo;
+          scan[kListTiles + jj] = hi;
+          scan[2 * kListTiles + jj] = neg;
+        }
+      }
+    }
+  };
+  // key tiles to scan: those that the CTA's last row may see (limits grow with the row).  The first ones by the
+  // warps that load no Q, meanwhile.
+  const int scan_n = kd ? min(kListTiles, (masked_limit(p, b, (min(row0 + 256, rows) - 1) / p.group, n) + 127) / 128) : 0;
+  const int scan_early = min(scan_n, 36);
+  if (warp >= 8) scan_ids(warp - 8, 4, scan_early);
+
   // the row threads: their warp's 32 rows of Q to smem (half a warp per row, 256 contiguous bytes, all loads on
   // their way at once), and what their own row sees
   const int row = row0 + int(threadIdx.x);
@@ -572,61 +616,47 @@ __global__ void __launch_bounds__(many::kThreads, 1)
   __syncthreads();
   const int tiles_a = (lim_max[0] + 127) / 128, tiles_b = (lim_max[1] + 127) / 128;  // key tiles that any of their rows may see
   const int full_a = lim_min[0] / 128, full_b = lim_min[1] / 128;                    // ... that all see, by their limits
-  const int* kd = p.k_doc ? p.k_doc + size_t(b) * p.kv_len : nullptr;
   const int tiles = max(tiles_a, tiles_b);
   const int my_j0 = int(static_cast<long long>(rank) * tiles / splits);
   const int my_j1 = int(static_cast<long long>(rank + 1) * tiles / splits);
-  // key tile states per row tile, 2 bits each: 0 no row sees any key, 1 every row sees every key, 2 between
   if (kd) {
-    for (int w = threadIdx.x; w < 2 * kListWords; w += kThreads) list[w] = 0;
-    __syncthreads();
-    constexpr int kWarps = kThreads / 32, kAhead = 3;  // tiles of ids in flight per warp
-    for (int j = my_j0 + warp; j < my_j1 && j < kListTiles; j += kWarps * kAhead) {
-      int d[kAhead][4];
+    if (scan_early < scan_n) {
+      scan_ids(scan_early + warp, kThreads / 32, scan_n);
+      __syncthreads();
+    }
+    for (int j0 = warp * 32; j0 < scan_n; j0 += kThreads) {
+      const int j = j0 + lane, jj = min(j, scan_n - 1);
+      const int lo = scan[jj], hi = scan[kListTiles + jj], neg = scan[2 * kListTiles + jj];
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int key = (j + u * kWarps) * 128 + e * 32 + lane;
-          d[u][e] = key < n ? __ldg(kd + key) : -1;
-        }
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int jj = j + u * kWarps;
-        int lo = 0x7fffffff, hi = -1, neg = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (d[u][e] < 0) neg = 1;
-          else lo = min(lo, d[u][e]);
-          hi = max(hi, d[u][e]);
-        }
-        lo = __reduce_min_sync(0xffffffffu, lo);
-        hi = __reduce_max_sync(0xffffffffu, hi);
-        neg = __reduce_max_sync(0xffffffffu, neg);
-        if (lane < 2 && jj < my_j1 && jj < kListTiles) {
-          const int t = lane;
-          const bool none = hi < doc_min[t] || lo > doc_max[t] || jj >= (t ? tiles_b : tiles_a);
-          const bool full = !neg && !doc_neg[t] && lo == hi && lo == doc_min[t] && lo == doc_max[t] &&
-                            jj < (t ? full_b : full_a);
-          if (!none) atomicOr(list + t * kListWords + (jj >> 4), (full ? 1u : 2u) << (2 * (jj & 15)));
+      for (int t = 0; t < 2; ++t) {
+        const bool some = j < (t ? tiles_b : tiles_a) && hi >= doc_min[t] && lo <= doc_max[t];
+        const bool every = !neg && !doc_neg[t] && lo == hi && lo == doc_min[t] && lo == doc_max[t] && j < (t ? full_b : full_a);
+        const uint32_t ws = __ballot_sync(0xffffffffu, some), wf = __ballot_sync(0xffffffffu, every);
+        if (lane == 0) {
+          seen[t * kListWords + j0 / 32] = ws;
+          full[t * kListWords + j0 / 32] = wf;
         }
       }
     }
+    fence_proxy_async_smem();  // the scan's place goes to the TMA loads
     __syncthreads();
   }
+  // what row tile t sees of key tile j: 0 nothing, 1 every row every key, 2 between
   auto state = [&](int t, int j) -> uint32_t {
     if (j >= (t ? tiles_b : tiles_a)) return 0u;
-    if (kd) return j < kListTiles ? (list[t * kListWords + (j >> 4)] >> (2 * (j & 15))) & 3u : 2u;
-    return j < (t ? full_b : full_a) ? 1u : 2u;
+    if (!kd) return j < (t ? full_b : full_a) ? 1u : 2u;
+    if (j >= kListTiles) return 2u;
+    const int w = t * kListWords + (j >> 5);
+    return seen[w] >> (j & 31) & 1u ? (full[w] >> (j & 31) & 1u ? 1u : 2u) : 0u;
   };
   // the next key tile of this CTA at or after j that some row of the row tiles in `which` (bit 0 A, bit 1 B) sees;
   // at or past my_j1: none
   auto next = [&](int j, int which) -> int {
     if (kd) {
       while (j < my_j1 && j < kListTiles) {
-        const uint32_t w = ((which & 1 ? list[j >> 4] : 0u) | (which & 2 ? list[kListWords + (j >> 4)] : 0u)) >> (2 * (j & 15));
-        if (w) return j + (__ffs(w) - 1) / 2;
-        j = (j | 15) + 1;
+        const uint32_t w = ((which & 1 ? seen[j >> 5] : 0u) | (which & 2 ? seen[kListWords + (j >> 5)] : 0u)) >> (j & 31);
+        if (w) return j + __ffs(w) - 1;
+        j = (j | 31) + 1;
       }
     }
     return j;
@@ -663,7 +693,7 @@ __global__ void __launch_bounds__(many::kThreads, 1)
         }
       }
     } else if (warp == 9) {
-if (lane == 0 && first < my_j1) {
+      if (lane == 0 && first < my_j1) {
         constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
         constexpr uint32_t idesc_o = idesc_bf16_f32(128, 128, false, true);
         auto issue_s = [&](int t, int it) {
@@ -744,7 +774,7 @@ if (lane == 0 && first < my_j1) {
             dirty |= (key >= n || (kd && __ldg(kd + key) < 0) ? 1u : 0u) << e;
           }
         }
-        if (!mbar_wait(&v_full[it & 1], (uint32_t(it) >> 1) & 1u, abort_flag, ZI_DEVERR_TIMEOUT_SOFTMAX)) break;
+        if (!mbar_wait_warp(&v_full[it & 1], (uint32_t(it) >> 1) & 1u, abort_flag, ZI_DEVERR_TIMEOUT_SOFTMAX)) break;
         if (__any_sync(0xffffffffu, dirty != 0)) {
           uint8_t* v = smem + kV0 + (it & 1) * kTile;
 #pragma unroll
@@ -811,7 +841,7 @@ if (lane == 0 && first < my_j1) {
             id[w] = key < n ? __ldg(kd + key) : -1;
           }
         }
-        if (!mbar_wait(&s_full[t], uint32_t(it) & 1u, abort_flag, ZI_DEVERR_TIMEOUT_SOFTMAX)) {
+        if (!mbar_wait_warp(&s_full[t], uint32_t(it) & 1u, abort_flag, ZI_DEVERR_TIMEOUT_SOFTMAX)) {
           ok = false;
           break;
         }
@@ -822,14 +852,14 @@ if (lane == 0 && first < my_j1) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) reg_fence32(&s[c * 32]);
         if constexpr (CAP) {
-          // |z| within the polynomial's range over the warp's rows, or (scores near the cap and past it) through
+          // |z| within the polynomial's range over the row's keys, or (scores near the cap and past it) through
           // exp and a reciprocal.  A NaN, of a key row that nobody sees, stays in its column and is masked below.
           float mx4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int c = 0; c < 128; c += 2)
             mx4[c / 2 & 3] = max3f(mx4[c / 2 & 3], fabsf(__uint_as_float(s[c])), fabsf(__uint_as_float(s[c + 1])));
           const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-          if (p.cap_poly && __all_sync(0xffffffffu, mx * p.scale_log2 <= kCapRange)) {
+          if (p.cap_poly && mx * p.scale_log2 <= kCapRange) {
 #pragma unroll
             for (int c = 0; c < 64; ++c) {
               float y0, y1;
@@ -929,7 +959,7 @@ if (lane == 0 && first < my_j1) {
           l += ((a0 + a1) + (b0 + b1)) + ((c0 + c1) + (d0 + d1));
         }
         if (resc && it > 0) {
-          if (!mbar_wait(&pv_done[t], uint32_t(it - 1) & 1u, abort_flag, ZI_DEVERR_TIMEOUT_SOFTMAX)) {
+          if (!mbar_wait_warp(&pv_done[t], uint32_t(it - 1) & 1u, abort_flag, ZI_DEVERR_TIMEOUT_SOFTMAX)) {
             ok = false;
             break;
           }
@@ -958,7 +988,7 @@ if (lane == 0 && first < my_j1) {
         ++it;
       }
       if (ok && it > 0) {
-        ok = mbar_wait(&pv_done[t], uint32_t(it - 1) & 1u, abort_flag, ZI_DEVERR_TIMEOUT_SOFTMAX);
+        ok = mbar_wait_warp(&pv_done[t], uint32_t(it - 1) & 1u, abort_flag, ZI_DEVERR_TIMEOUT_SOFTMAX);
         if (ok) tc_fence_after();
       }
     }
@@ -967,6 +997,9 @@ if (lane == 0 && first < my_j1) {
     if (splits == 1) {
       const float inv = m_run == -INFINITY ? 0.f : 1.0f / l;  // a row that sees no key: zeros
       if (ok) {
+        // Through this warp's quarter of its tile's Q (read for the last time by an MMA that is done), so that half a
+        // warp stores a row's 256 bytes: a thread storing its own row touches 32 lines with every instruction
+        uint8_t* stage = smem + kQ0 + t * kTile + q * 8192;
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t o[32];
@@ -974,13 +1007,21 @@ if (lane == 0 && first < my_j1) {
           float f[32];
 #pragma unroll
           for (int k = 0; k < 32; ++k) f[k] = it > 0 ? __uint_as_float(o[k]) * inv : 0.f;
-          if (live) {
-            uint4* d = reinterpret_cast<uint4*>(orow + c * 32);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              d[k] = make_uint4(pack_bf16x2(f[8 * k], f[8 * k + 1]), pack_bf16x2(f[8 * k + 2], f[8 * k + 3]),
-                                pack_bf16x2(f[8 * k + 4], f[8 * k + 5]), pack_bf16x2(f[8 * k + 6], f[8 * k + 7]));
-          }
+          for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<uint4*>(stage + lane * 256 + (((c * 4 + k) ^ (lane & 7)) << 4)) =
+                make_uint4(pack_bf16x2(f[8 * k], f[8 * k + 1]), pack_bf16x2(f[8 * k + 2], f[8 * k + 3]),
+                           pack_bf16x2(f[8 * k + 4], f[8 * k + 5]), pack_bf16x2(f[8 * k + 6], f[8 * k + 7]));
+        }
+        __syncwarp();
+        const long long at = orow - p.out;
+        const int x = lane & 15, left = rows - (row - lane);  // rows of the warp that exist
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int r = 2 * e + (lane >> 4);
+          const long long to = __shfl_sync(0xffffffffu, at, r);
+          const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 256 + ((x ^ (r & 7)) << 4));
+          if (r < left) *reinterpret_cast<uint4*>(p.out + to + x * 8) = w;
         }
       }
     } else {

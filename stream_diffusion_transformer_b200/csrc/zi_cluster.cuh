@@ -1,9 +1,17 @@
-// Reading the shared memory of a cluster's other CTAs.  The loads are predicated rather than
-// branched around, so that those of all ranks are on their way together.
+// Waits of whole warps, and reading the shared memory of a cluster's other CTAs.
 #pragma once
 #include "zi_common.cuh"
 
 namespace zi {
+
+// mbar_wait by all 32 lanes with one answer: a lane that gives up takes its warp along, so that no
+// other lane waits for it in a later warp-wide instruction.
+ZI_DEV bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned int code) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, code));
+}
+
+// Loads from peers are predicated rather than branched around, so that those of all ranks are on
+// their way together.
 
 constexpr int kMaxCluster = 8;
 

@@ -894,7 +894,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
     while (ok && walk.next(wi)) {
       for (int kb = 0; kb < sched.kb; ++kb, ++it) {
         const uint32_t s = it % kStages, r = it / kStages;
-        if (!mbar_wait(&sc_full[s], r & 1u, abort_flag, ZI_DEVERR_TIMEOUT_EPILOGUE)) {
+        if (!mbar_wait_warp(&sc_full[s], r & 1u, abort_flag, ZI_DEVERR_TIMEOUT_EPILOGUE)) {
           ok = false;
           break;
         }
@@ -921,7 +921,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
     int local = 0;
     WorkWalker walk(sched, unit);
     while (!err && walk.next(wi)) {
-      if (!mbar_wait(tfull, uint32_t(local) & 1u, abort_flag, ZI_DEVERR_TIMEOUT_EPILOGUE)) break;
+      if (!mbar_wait_warp(tfull, uint32_t(local) & 1u, abort_flag, ZI_DEVERR_TIMEOUT_EPILOGUE)) break;
       ++local;
       tc_fence_after();
       uint32_t v[128];

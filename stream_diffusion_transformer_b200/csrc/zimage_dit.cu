@@ -1182,6 +1182,9 @@ int zi_attention_masked(const zi_attention_desc* d, zi_stream_t stream) {
   if (!d || d->batch <= 0 || d->heads <= 0 || d->kv_heads <= 0 || d->q_len <= 0 || d->kv_len <= 0) return ZI_ERR_ARG;
   if (!(d->scale > 0.f) || !std::isfinite(d->scale) || !(d->softcap >= 0.f) || !std::isfinite(d->softcap))
     return ZI_ERR_ARG;
+  // products and quotients of these and of distances up to 2^24 stay in fp32's range
+  const double lo = std::ldexp(1.0, -60), hi = std::ldexp(1.0, 60);
+  if (d->scale < lo || d->scale > hi || (d->softcap > 0.f && (d->softcap < lo || d->softcap > hi))) return ZI_ERR_ARG;
   if ((d->causal != 0 && d->causal != 1) || (d->d_prefix_len && !d->causal)) return ZI_ERR_ARG;
   if ((d->d_q_doc == nullptr) != (d->d_k_doc == nullptr)) return ZI_ERR_ARG;
   if (d->heads % d->kv_heads) return ZI_ERR_SHAPE;

@@ -220,6 +220,52 @@ def test_scores_far_out():
     check(q, k, v, slopes=torch.tensor([40.0, 0.0], device="cuda"), causal=True)
 
 
+def test_scales_and_caps_at_the_ends_of_their_range():
+    for n, m in ((2, 100), (300, 400)):
+        q, k, v = inputs(1, n, m, 2, 1, 10)
+        for kw in (dict(scale=2.0 ** -60), dict(softcap=2.0 ** -60), dict(softcap=2.0 ** 60), dict(scale=2.0 ** -60, softcap=2.0 ** 60),
+                   dict(scale=2.0 ** -60, slopes=slopes_of(2)), dict(softcap=2.0 ** 60, slopes=slopes_of(2))):
+            check(q, k, v, causal=True, **kw)
+
+
+def test_documents_past_the_lists_of_key_tiles():
+    """More key tiles (2,110) than the kernel lists by document: the later ones are masked one by one."""
+    n, m = 300, 270000
+    q, k, v = inputs(1, n, m, 1, 1, 11)
+    ids = (torch.arange(m, dtype=torch.int32, device="cuda") // 90000)[None].contiguous()
+    q_ids = torch.full((1, n), 2, dtype=torch.int32, device="cuda")
+    q_ids[:, :20], q_ids[:, 20:40] = 0, 7
+    got = check(q, k, v, q_doc=q_ids, k_doc=ids, kv_len=i32(m - 77), causal=True)
+    assert (got[0, 20:40] == 0).all()
+
+
+def test_first_call_of_a_process_may_be_captured():
+    """Each kernel's first launch raises its shared-memory limit; that may happen while a stream is being captured."""
+    import subprocess
+    import sys
+    from conftest import ROOT
+    code = """
+import torch
+from stream_diffusion_transformer_b200 import model
+x, w = torch.randn(700, 256, device="cuda"), torch.randn(264, 256, device="cuda")
+q = torch.randn(1, 300, 2, 128, device="cuda").bfloat16()
+torch.cuda.synchronize()
+def run():
+    a, b = model.quantize_fp4(x), model.quantize_fp4(w)
+    return (model.gemm_fp4(a, b), model.gemm_fp4(model.quantize_fp4(x[:5]), b), model.attention_masked(q, q, q, softcap=9.0),
+            model.attention_masked(q[:, :2], q, q))
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = run()
+g.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, run()))
+print("same")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
+
+
 def test_streams_graphs_and_repeats():
     """The same bits on another stream, from a captured graph on new inputs, and with two calls at once."""
     from stream_diffusion_transformer_b200 import model

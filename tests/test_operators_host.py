@@ -110,9 +110,9 @@ def test_masked_attention(abi):
     bad(abi.ZI_ERR_SHAPE, q_len=(1 << 24) + 1)
     bad(abi.ZI_ERR_SHAPE, kv_len=(1 << 24) + 1)
     bad(abi.ZI_ERR_SHAPE, heads=256, kv_heads=1, q_len=1 << 23)
-    for v in (0.0, -1.0, float("nan"), float("inf")):
+    for v in (0.0, -1.0, float("nan"), float("inf"), 1e-19, 2e18):
         bad(abi.ZI_ERR_ARG, scale=v)
-    for v in (-1.0, float("nan"), float("inf")):
+    for v in (-1.0, float("nan"), float("inf"), 1e-40, 1e-19, 2e18):
         bad(abi.ZI_ERR_ARG, softcap=v)
     bad(abi.ZI_ERR_ARG, causal=2)
     bad(abi.ZI_ERR_ARG, d_prefix_len=P)
