@@ -442,7 +442,7 @@ ZI_DEV uint64_t desc_at(uint32_t low, uint32_t bytes) {
   return d;
 }
 
-template <bool CAP, bool BIAS>
+template <bool CAP, bool BIAS, bool DOC>
 __global__ void __launch_bounds__(many::kThreads, 1)
     attention_many_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                           MaskedParams p, int splits) {
@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(many::kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const bool skip = *abort_flag != 0;
 
-  const int* kd = p.k_doc ? p.k_doc + size_t(b) * p.kv_len : nullptr;
+  const int* kd = DOC ? p.k_doc + size_t(b) * p.kv_len : nullptr;
   int* scan = reinterpret_cast<int*>(smem + kScan);
   // Ranges of the document ids of key tiles first, first + step, ... below end; three tiles' loads on their way per warp
   auto scan_ids = [&](int first, int step, int end) {
@@ -559,9 +559,9 @@ __global__ void __launch_bounds__(many::kThreads, 1)
   };
   // key tiles to scan: those that the CTA's last row may see (limits grow with the row).  The first ones by the
   // warps that load no Q, meanwhile.
-  const int scan_n = kd ? min(kListTiles, (masked_limit(p, b, (min(row0 + 256, rows) - 1) / p.group, n) + 127) / 128) : 0;
+  const int scan_n = DOC ? min(kListTiles, (masked_limit(p, b, (min(row0 + 256, rows) - 1) / p.group, n) + 127) / 128) : 0;
   const int scan_early = min(scan_n, 36);
-  if (warp >= 8) scan_ids(warp - 8, 4, scan_early);
+  if (DOC && warp >= 8) scan_ids(warp - 8, 4, scan_early);
 
   // the row threads: their warp's 32 rows of Q to smem (half a warp per row, 256 contiguous bytes, all loads on
   // their way at once), and what their own row sees
@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(many::kThreads, 1)
     int d_lo = 0x7fffffff, d_hi = -1, neg = 0;
     if (have) {
       lim = masked_limit(p, b, qi, n);
-      if (p.q_doc) {
+      if (DOC) {
         doc = __ldg(p.q_doc + size_t(b) * p.q_len + qi);
         if (doc < 0) {
           lim = 0;
@@ -619,7 +619,7 @@ __global__ void __launch_bounds__(many::kThreads, 1)
   const int tiles = max(tiles_a, tiles_b);
   const int my_j0 = int(static_cast<long long>(rank) * tiles / splits);
   const int my_j1 = int(static_cast<long long>(rank + 1) * tiles / splits);
-  if (kd) {
+  if constexpr (DOC) {
     if (scan_early < scan_n) {
       scan_ids(scan_early + warp, kThreads / 32, scan_n);
       __syncthreads();
@@ -644,7 +644,7 @@ __global__ void __launch_bounds__(many::kThreads, 1)
   // what row tile t sees of key tile j: 0 nothing, 1 every row every key, 2 between
   auto state = [&](int t, int j) -> uint32_t {
     if (j >= (t ? tiles_b : tiles_a)) return 0u;
-    if (!kd) return j < (t ? full_b : full_a) ? 1u : 2u;
+    if (!DOC) return j < (t ? full_b : full_a) ? 1u : 2u;
     if (j >= kListTiles) return 2u;
     const int w = t * kListWords + (j >> 5);
     return seen[w] >> (j & 31) & 1u ? (full[w] >> (j & 31) & 1u ? 1u : 2u) : 0u;
@@ -652,7 +652,7 @@ __global__ void __launch_bounds__(many::kThreads, 1)
   // the next key tile of this CTA at or after j that some row of the row tiles in `which` (bit 0 A, bit 1 B) sees;
   // at or past my_j1: none
   auto next = [&](int j, int which) -> int {
-    if (kd) {
+    if constexpr (DOC) {
       while (j < my_j1 && j < kListTiles) {
         const uint32_t w = ((which & 1 ? seen[j >> 5] : 0u) | (which & 2 ? seen[kListWords + (j >> 5)] : 0u)) >> (j & 31);
         if (w) return j + __ffs(w) - 1;
@@ -662,7 +662,7 @@ __global__ void __launch_bounds__(many::kThreads, 1)
     return j;
   };
   const int first = skip ? my_j1 : next(my_j0, 3);
-  const bool clean = p.lengths != nullptr || kd != nullptr;  // V may hold rows that nobody sees
+  const bool clean = DOC || p.lengths != nullptr;  // V may hold rows that nobody sees
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
@@ -771,7 +771,7 @@ __global__ void __launch_bounds__(many::kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int key = j * 128 + e * 32 + lane;
-            dirty |= (key >= n || (kd && __ldg(kd + key) < 0) ? 1u : 0u) << e;
+            dirty |= (key >= n || (DOC && __ldg(kd + key) < 0) ? 1u : 0u) << e;
           }
         }
         if (!mbar_wait_warp(&v_full[it & 1], (uint32_t(it) >> 1) & 1u, abort_flag, ZI_DEVERR_TIMEOUT_SOFTMAX)) break;
@@ -834,7 +834,7 @@ __global__ void __launch_bounds__(many::kThreads, 1)
       for (int j = next(my_j0, mine); ok && j < stop; j = next(j + 1, mine)) {
         const bool part = state(t, j) != 1;
         int id[4];  // document ids of keys w 32 + lane, on their way while S is computed
-        if (kd && part) {
+        if (DOC && part) {
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             const int key = j * 128 + w * 32 + lane;
@@ -859,7 +859,8 @@ __global__ void __launch_bounds__(many::kThreads, 1)
           for (int c = 0; c < 128; c += 2)
             mx4[c / 2 & 3] = max3f(mx4[c / 2 & 3], fabsf(__uint_as_float(s[c])), fabsf(__uint_as_float(s[c + 1])));
           const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-          if (p.cap_poly && mx * p.scale_log2 <= kCapRange) {
+          const bool near = p.cap_poly && mx * p.scale_log2 <= kCapRange;
+          if (__all_sync(0xffffffffu, near)) {
 #pragma unroll
             for (int c = 0; c < 64; ++c) {
               float y0, y1;
@@ -867,10 +868,15 @@ __global__ void __launch_bounds__(many::kThreads, 1)
               s[2 * c] = __float_as_uint(y0);
               s[2 * c + 1] = __float_as_uint(y1);
             }
-          } else {
+          } else {  // some row of the warp needs the other way; each takes its own, whatever its neighbours hold
 #pragma unroll
-            for (int c = 0; c < 128; ++c)
-              s[c] = __float_as_uint(tanh_exp(__uint_as_float(s[c]) * p.scale_log2) * p.cap_log2);
+            for (int c = 0; c < 64; ++c) {
+              const float s0 = __uint_as_float(s[2 * c]), s1 = __uint_as_float(s[2 * c + 1]);
+              float y0, y1;
+              f2_unpack(cap_poly_pair(f2_pack(s0, s1), cc), y0, y1);
+              s[2 * c] = __float_as_uint(near ? y0 : tanh_exp(s0 * p.scale_log2) * p.cap_log2);
+              s[2 * c + 1] = __float_as_uint(near ? y1 : tanh_exp(s1 * p.scale_log2) * p.cap_log2);
+            }
           }
         }
         float base = 0.f;  // what every score of the row in this tile still lacks, in the exp2 domain
@@ -895,7 +901,7 @@ __global__ void __launch_bounds__(many::kThreads, 1)
           const int left = lim - j * 128;
 #pragma unroll
           for (int w = 0; w < 4; ++w) vis[w] = left >= 32 * w + 32 ? ~0u : left <= 32 * w ? 0u : (1u << (left - 32 * w)) - 1u;
-          if (kd) {
+          if constexpr (DOC) {
             for (uint32_t todo = ~0u; todo;) {  // once for each document among the warp's rows
               const int d = __shfl_sync(0xffffffffu, doc, __ffs(todo) - 1);
               todo &= ~__ballot_sync(0xffffffffu, doc == d);

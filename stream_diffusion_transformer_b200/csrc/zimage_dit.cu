@@ -8,6 +8,7 @@
 #include <cmath>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 #include <vector>
 
 #include "zi_attention.cuh"
@@ -883,12 +884,12 @@ int run_attention_few(DevInfo* dev, const MaskedParams& p, cudaStream_t st) {
 // (65 MB), where the longest units should start first, 178 / 245 us.
 constexpr long long kHeadGroupBytes = 72LL << 20;
 
-template <bool CAP, bool BIAS>
+template <bool CAP, bool BIAS, bool DOC>
 int run_attention_many(DevInfo* dev, MaskedParams p, cudaStream_t st) {
   CUtensorMap tk, tv;
   ZI_TRY(make_kv_map(&tk, p.k, p.k_bs, p.k_rs, p.k_hs, p.batch, p.kv_len, p.kv_heads, 128));
   ZI_TRY(make_kv_map(&tv, p.v, p.v_bs, p.v_rs, p.v_hs, p.batch, p.kv_len, p.kv_heads, 128));
-  constexpr auto kern = attention_many_kernel<CAP, BIAS>;
+  constexpr auto kern = attention_many_kernel<CAP, BIAS, DOC>;
   ZI_TRY((raise_smem<kern>(dev, int(many::kSmemBytes))));
   const long long x = (static_cast<long long>(p.q_len) * p.group + 255) / 256;
   const long long units = x * p.kv_heads * p.batch;
@@ -922,9 +923,13 @@ bool prefer_few(const DevInfo* dev, const MaskedParams& p) {
 
 int run_attention_masked(DevInfo* dev, const MaskedParams& p, cudaStream_t st) {
   if (prefer_few(dev, p)) return run_attention_few(dev, p, st);
-  if (p.cap_log2 != 0.f)
-    return p.slopes ? run_attention_many<true, true>(dev, p, st) : run_attention_many<true, false>(dev, p, st);
-  return p.slopes ? run_attention_many<false, true>(dev, p, st) : run_attention_many<false, false>(dev, p, st);
+  auto run = [&](auto doc) {
+    constexpr bool kDoc = decltype(doc)::value;
+    if (p.cap_log2 != 0.f)
+      return p.slopes ? run_attention_many<true, true, kDoc>(dev, p, st) : run_attention_many<true, false, kDoc>(dev, p, st);
+    return p.slopes ? run_attention_many<false, true, kDoc>(dev, p, st) : run_attention_many<false, false, kDoc>(dev, p, st);
+  };
+  return p.k_doc ? run(std::true_type{}) : run(std::false_type{});
 }
 
 // Checks one operand's strides; those of dimensions of size 1 are not read and become 0.

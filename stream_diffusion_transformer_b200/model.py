@@ -454,15 +454,23 @@ class Fp4Matrix(NamedTuple):
 _FP4_FORMATS = {"mxfp4": abi.ZI_FP4_MX, "nvfp4": abi.ZI_FP4_NV}
 
 
+_current_device = torch.cuda.current_device
+
+
+def _raw_stream(device: int) -> int:
+    """The current stream of GPU `device` as the address of its cudaStream_t."""
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
 def _launch(device: int, fn: str, *args) -> None:
     """abi.call with the current stream of GPU `device` as its last argument, and that GPU current.  A few
     microseconds of host time are as long as the smallest kernels here, so the common case (the GPU is
     current already) enters no context and builds no stream object."""
-    if torch.cuda.current_device() == device:
-        abi.call(fn, *args, torch._C._cuda_getCurrentRawStream(device))
+    if _current_device() == device:
+        abi.call(fn, *args, _raw_stream(device))
     else:
         with torch.cuda.device(device):
-            abi.call(fn, *args, torch._C._cuda_getCurrentRawStream(device))
+            abi.call(fn, *args, _raw_stream(device))
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -482,14 +490,15 @@ def _fp4_scale_bytes(f: int, rows: int, cols: int) -> int:
     return -(-rows // 128) * -(-cols // per) * 512
 
 
-def _fp4_check(m: Fp4Matrix) -> int:
-    """The library's number of m's format, after checking m's tensors (the library sees pointers only)."""
-    f = _fp4_format(m.fmt)
-    q, bs, rs = m.codes, m.block_scales, m.row_scales
-    if q.dim() != 2 or q.dtype != torch.uint8 or not q.is_cuda or not q.is_contiguous():
+def _fp4_check(m: Fp4Matrix):
+    """(format number, rows, columns, GPU index) of m, after checking m's tensors (the library sees pointers only)."""
+    fmt, q, bs, rs = m
+    f = _fp4_format(fmt)
+    shape, device = q.shape, q.get_device()
+    if len(shape) != 2 or q.dtype != torch.uint8 or device < 0 or not q.is_contiguous():
         raise ValueError("codes: a contiguous 2-D uint8 tensor on a GPU is needed")
-    rows, device = q.shape[0], q.get_device()
-    n = _fp4_scale_bytes(f, rows, 2 * q.shape[1])
+    rows, cols = shape[0], 2 * shape[1]
+    n = _fp4_scale_bytes(f, rows, cols)
     if bs.dtype != torch.uint8 or not bs.is_contiguous() or bs.get_device() != device or bs.numel() != n:
         raise ValueError(f"block_scales: a contiguous uint8 tensor of {n} elements on the codes' GPU is needed")
     if (rs is not None) != (f == abi.ZI_FP4_NV):
@@ -497,47 +506,46 @@ def _fp4_check(m: Fp4Matrix) -> int:
     if rs is not None and (rs.dtype != torch.float32 or not rs.is_contiguous() or rs.get_device() != device
                            or rs.numel() != rows):
         raise ValueError(f"row_scales: a contiguous fp32 tensor of {rows} elements on the codes' GPU is needed")
-    return f
+    return f, rows, cols, device
 
 
 def quantize_fp4(x: torch.Tensor, fmt: str = "nvfp4") -> Fp4Matrix:
     """The rows of a 2-D fp32 or bf16 tensor in 4 bits (zi_quantize_fp4)."""
     f = _fp4_format(fmt)
-    bf16 = x.dtype == torch.bfloat16
-    if x.dim() != 2 or not x.is_cuda or not x.is_contiguous() or not (bf16 or x.dtype == torch.float32):
+    shape, dtype = x.shape, x.dtype
+    if len(shape) != 2 or not x.is_cuda or not x.is_contiguous() or dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("quantize_fp4: a contiguous 2-D fp32 or bf16 tensor on a GPU is needed")
-    rows, cols = x.shape
-    q = x.new_empty((rows, cols // 2), dtype=torch.uint8)
-    bs = x.new_empty(_fp4_scale_bytes(f, rows, cols), dtype=torch.uint8)
-    rs = x.new_empty(rows, dtype=torch.float32) if f == abi.ZI_FP4_NV else None
+    rows, cols = shape
+    device = x.device
+    q = torch.empty(rows, cols // 2, dtype=torch.uint8, device=device)
+    bs = torch.empty(_fp4_scale_bytes(f, rows, cols), dtype=torch.uint8, device=device)
+    rs = torch.empty(rows, dtype=torch.float32, device=device) if f == abi.ZI_FP4_NV else None
     if rows:
-        _launch(x.get_device(), "zi_quantize_fp4", f, x.data_ptr(), 1 if bf16 else 0, rows, cols, q.data_ptr(),
-                bs.data_ptr(), _ptr(rs))
+        _launch(device.index, "zi_quantize_fp4", f, x.data_ptr(), 1 if dtype == torch.bfloat16 else 0, rows, cols,
+                q.data_ptr(), bs.data_ptr(), _ptr(rs))
     return Fp4Matrix(fmt, q, bs, rs)
 
 
 def dequantize_fp4(m: Fp4Matrix, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
     """The values that a 4-bit matrix stands for, bf16 or fp32 [rows, cols] (zi_dequantize_fp4)."""
-    f = _fp4_check(m)
+    f, rows, cols, device = _fp4_check(m)
     if dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("dequantize_fp4: fp32 or bf16")
-    rows, cols = m.shape
-    y = m.codes.new_empty((rows, cols), dtype=dtype)
+    y = torch.empty(rows, cols, dtype=dtype, device=m.codes.device)
     if rows:
-        _launch(y.get_device(), "zi_dequantize_fp4", f, m.codes.data_ptr(), m.block_scales.data_ptr(),
-                _ptr(m.row_scales), rows, cols, y.data_ptr(), 1 if dtype == torch.bfloat16 else 0)
+        _launch(device, "zi_dequantize_fp4", f, m.codes.data_ptr(), m.block_scales.data_ptr(), _ptr(m.row_scales), rows,
+                cols, y.data_ptr(), 1 if dtype == torch.bfloat16 else 0)
     return y
 
 
 def gemm_fp4(a: Fp4Matrix, b: Fp4Matrix, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """bf16 [M, N] = a [M, K] b [N, K]^T of two 4-bit matrices of one format (zi_gemm_fp4)."""
-    f = _fp4_check(a)
-    (M, K), (N, Kb) = a.shape, b.shape
-    device = a.codes.get_device()
-    if _fp4_check(b) != f or K != Kb or b.codes.get_device() != device:
+    f, M, K, device = _fp4_check(a)
+    fb, N, Kb, device_b = _fp4_check(b)
+    if fb != f or K != Kb or device_b != device:
         raise ValueError("gemm_fp4: two matrices of one format, one K and one device are needed")
     if out is None:
-        out = a.codes.new_empty((M, N), dtype=torch.bfloat16)
+        out = torch.empty(M, N, dtype=torch.bfloat16, device=a.codes.device)
     elif (tuple(out.shape) != (M, N) or out.dtype != torch.bfloat16 or not out.is_contiguous()
           or out.get_device() != device):
         raise ValueError("gemm_fp4: out has to be a contiguous bf16 [M, N] tensor on the operands' GPU")
@@ -560,12 +568,12 @@ def attention_masked(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, scale
     if q.dim() != 4 or k.dim() != 4 or k.shape != v.shape or q.shape[0] != k.shape[0] or q.shape[3] != 128 \
             or k.shape[3] != 128:
         raise ValueError("attention_masked: q [B, q_len, H, 128] and k, v [B, kv_len, Hk, 128] are needed")
-    if out is None:
-        out = q.new_empty(q.shape)
-    elif out.shape != q.shape:
-        raise ValueError("attention_masked: out has to have q's shape")
     B, n, H, _ = q.shape
     m, Hk = k.shape[1], k.shape[2]
+    if out is None:
+        out = torch.empty(B, n, H, 128, dtype=torch.bfloat16, device=q.device)
+    elif out.shape != q.shape:
+        raise ValueError("attention_masked: out has to have q's shape")
     device = q.get_device()
     strides = []
     for name, t in (("q", q), ("k", k), ("v", v), ("out", out)):
@@ -573,15 +581,18 @@ def attention_masked(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, scale
         if t.dtype != torch.bfloat16 or not t.is_cuda or t.get_device() != device or st[3] != 1:
             raise ValueError(f"attention_masked: {name} has to be bf16 with contiguous heads on q's GPU")
         strides += st[:3]
-    for name, t, dtype, shape in (("slopes", slopes, torch.float32, (H,)), ("prefix_len", prefix_len, torch.int32, (B,)),
-                                  ("kv_len", kv_len, torch.int32, (B,)), ("q_doc", q_doc, torch.int32, (B, n)),
-                                  ("k_doc", k_doc, torch.int32, (B, m))):
-        if t is not None and (t.dtype != dtype or t.shape != shape or not t.is_contiguous()
-                              or t.get_device() != device):
+    def small(name, t, dtype, *shape):
+        if t is None:
+            return None
+        if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
             raise ValueError(f"attention_masked: {name} has to be a contiguous {dtype} tensor {shape} on q's GPU")
+        return t.data_ptr()
+
     d = abi.ZiAttentionDesc(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), *strides, B, H, Hk, n, m,
-                            128 ** -0.5 if scale is None else scale, softcap, _ptr(slopes), 1 if causal else 0,
-                            _ptr(prefix_len), _ptr(kv_len), _ptr(q_doc), _ptr(k_doc))
+                            128 ** -0.5 if scale is None else scale, softcap, small("slopes", slopes, torch.float32, H),
+                            1 if causal else 0, small("prefix_len", prefix_len, torch.int32, B),
+                            small("kv_len", kv_len, torch.int32, B), small("q_doc", q_doc, torch.int32, B, n),
+                            small("k_doc", k_doc, torch.int32, B, m))
     _launch(device, "zi_attention_masked", ctypes.byref(d))
     return out
 
