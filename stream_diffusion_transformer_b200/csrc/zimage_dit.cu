@@ -365,6 +365,9 @@ int launch_clustered(int kind, dim3 grid, int threads, uint32_t smem, int cluste
 // ---------------------------------------------------------------- 4-bit rows
 
 constexpr int kFp4MaxCols = 16384;
+// From this many rows on the rows alone fill the GPU, and fewer threads per row with more loads on their way each are
+// faster.  Measured with one and four 32-byte spans per thread: 20480 x 3840 bf16 to NVFP4 62.7 / 46.6 us, 4128 x
+// 3840 14.8 / 12.3.
 constexpr int kFp4DeepRows = 1024;
 constexpr int kMaxDim = 1 << 24;
 
@@ -379,7 +382,6 @@ template <int FMT, typename TIn>
 int run_quantize_fp4(const TIn* x, int rows, int cols, uint8_t* q, uint8_t* bs, float* rs, cudaStream_t st) {
   const int spans = cols / 16;
   int tpr = fp4_threads_per_row(cols), nb = (spans + tpr - 1) / tpr;
-  // Enough rows to fill the GPU: more spans per thread, so that more bytes are on their way at a time
   constexpr int kDeep = sizeof(TIn) == 4 ? 2 : 4;
   static_assert(kFp4MaxCols / 16 <= 4 * fp4::kRowsThreads, "at most 4 spans per thread");
   while (rows >= kFp4DeepRows && nb < kDeep && tpr > 8) {
