@@ -808,6 +808,9 @@ __global__ void __launch_bounds__(many::kThreads, 1)
     const uint32_t o_addr = lane_addr + kColO + 128 * t;
     float m_run = -INFINITY, l = 0.f;
     bool ok = !skip;
+    // A wait of this lane ran out: it goes on with what TMEM holds until the next vote, where its warp leaves together
+    // (a vote at each wait costs 3% of the kernel)
+    bool lost = false;
     int it = 0;
     {
       // scores are in the exp2 domain after a cap, and scaled into it by the exponential's argument without one
@@ -841,10 +844,7 @@ __global__ void __launch_bounds__(many::kThreads, 1)
             id[w] = key < n ? __ldg(kd + key) : -1;
           }
         }
-        if (!mbar_wait_warp(&s_full[t], uint32_t(it) & 1u, abort_flag, ZI_DEVERR_TIMEOUT_SOFTMAX)) {
-          ok = false;
-          break;
-        }
+        lost |= !mbar_wait(&s_full[t], uint32_t(it) & 1u, abort_flag, ZI_DEVERR_TIMEOUT_SOFTMAX);
         tc_fence_after();
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + c * 32, &s[c * 32]);
@@ -930,7 +930,11 @@ __global__ void __launch_bounds__(many::kThreads, 1)
         const float m_new = fmaxf(m_run, fmaf(mx, sl2, base));
         // each row moves its maximum by its own scores alone, so its result does not depend on its neighbours
         const bool grows = m_new > m_run + 8.0f;
-        const bool resc = __any_sync(0xffffffffu, grows);
+        const bool resc = __any_sync(0xffffffffu, grows || lost);
+        if (resc && __any_sync(0xffffffffu, lost)) {
+          ok = false;
+          break;
+        }
         float alpha = 1.0f;
         if (grows) {
           alpha = m_run == -INFINITY ? 0.f : fast_exp2(m_run - m_new);  // a row that has seen nothing yet holds nothing
@@ -965,10 +969,7 @@ __global__ void __launch_bounds__(many::kThreads, 1)
           l += ((a0 + a1) + (b0 + b1)) + ((c0 + c1) + (d0 + d1));
         }
         if (resc && it > 0) {
-          if (!mbar_wait_warp(&pv_done[t], uint32_t(it - 1) & 1u, abort_flag, ZI_DEVERR_TIMEOUT_SOFTMAX)) {
-            ok = false;
-            break;
-          }
+          lost |= !mbar_wait(&pv_done[t], uint32_t(it - 1) & 1u, abort_flag, ZI_DEVERR_TIMEOUT_SOFTMAX);
           tc_fence_after();
           const uint64_t a2 = f2_pack(alpha, alpha);
 #pragma unroll 1
@@ -994,7 +995,7 @@ __global__ void __launch_bounds__(many::kThreads, 1)
         ++it;
       }
       if (ok && it > 0) {
-        ok = mbar_wait_warp(&pv_done[t], uint32_t(it - 1) & 1u, abort_flag, ZI_DEVERR_TIMEOUT_SOFTMAX);
+        ok = !__any_sync(0xffffffffu, lost) && mbar_wait_warp(&pv_done[t], uint32_t(it - 1) & 1u, abort_flag, ZI_DEVERR_TIMEOUT_SOFTMAX);
         if (ok) tc_fence_after();
       }
     }

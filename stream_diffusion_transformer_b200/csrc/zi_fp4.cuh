@@ -750,7 +750,6 @@ ZI_DEV void wide_epilogue(uint32_t* v, int row0, int lane, int n0, int half, uin
       put(c, y);
     }
     flush(n0 / 2 + 64 * half, ep.ldo);
-    return;
   }
   if constexpr (EPI == EPI_QKV) {
     const int region = n0 / ep.dim;  // 0 = q, 1 = k, 2 = v
@@ -773,17 +772,19 @@ ZI_DEV void wide_epilogue(uint32_t* v, int row0, int lane, int n0, int half, uin
       }
     }
   }
+  if constexpr (EPI != EPI_SWIGLU) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < 2; ++h) {
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      if (EPI == EPI_BF16) scale8(8 * h + c);
-      float y[8];
+      for (int c = 0; c < 8; ++c) {
+        if (EPI == EPI_BF16) scale8(8 * h + c);
+        float y[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = f(64 * h + 8 * c + i);
-      put(c, y);
+        for (int i = 0; i < 8; ++i) y[i] = f(64 * h + 8 * c + i);
+        put(c, y);
+      }
+      flush(nb + 64 * h, EPI == EPI_BF16 ? p.N : ep.ldo);
     }
-    flush(nb + 64 * h, EPI == EPI_BF16 ? p.N : ep.ldo);
   }
 }
 
