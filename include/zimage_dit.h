@@ -383,10 +383,10 @@ ZI_API int zi_attention_varlen(const uint16_t* d_qkv, uint16_t* d_out, int batch
 
 /* One call of zi_attention_masked.  Tensors are bf16 with 128 contiguous elements per
  * head; q and out [batch, q_len, heads, 128], k and v [batch, kv_len, kv_heads, 128],
- * each with its own strides (in elements, multiples of 8; the stride of a dimension of
- * size 1 is not read), so slices of a fused projection, [batch, heads, rows, 128] layouts
- * and caches with room to grow are passed as they are.  zi_attention_desc_init gives a
- * desc with every optional field off. */
+ * each with its own strides (in elements, multiples of 8, at least 128: no broadcast
+ * dimensions; the stride of a dimension of size 1 is not read), so slices of a fused
+ * projection, [batch, heads, rows, 128] layouts and caches with room to grow are passed as
+ * they are.  zi_attention_desc_init gives a desc with every optional field off. */
 typedef struct zi_attention_desc {
   const uint16_t* q;
   const uint16_t* k;
@@ -424,6 +424,8 @@ ZI_API int zi_attention_desc_init(zi_attention_desc* desc);
  * attention.  The masks given apply together.  A query that sees no key (no keys, all
  * masked, a negative id) gets zeros.  fp32 scores and softmax, probabilities rounded to
  * bf16 for the second product, one rounding of the result.
+ * The scores of keys that are seen, cap and bias included, may be up to 2^29 in size (larger
+ * ones are further apart in fp32 than exp2 reaches: their rows may come out as NaN).
  * What key rows past an element's end and rows with a negative id hold is never used (NaN
  * included).  A key that some queries see has to be finite: the product of a masked
  * probability (zero) and a NaN or infinity in a seen row of v is NaN.

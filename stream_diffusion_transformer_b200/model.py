@@ -563,7 +563,8 @@ def attention_masked(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, scale
     """Attention with capped scores, a distance bias and masks (zi_attention_masked).
 
     q bf16 [B, q_len, H, 128], k and v bf16 [B, kv_len, Hk, 128] with H a multiple of Hk, in any
-    strides with contiguous heads; returns bf16 [B, q_len, H, 128].  softcap 0 = none; slopes fp32 [H];
+    strides with contiguous heads (multiples of 8, no broadcast dimensions); returns bf16
+    [B, q_len, H, 128].  softcap 0 = none; slopes fp32 [H];
     prefix_len (with causal) and kv_len int32 [B]; q_doc int32 [B, q_len] with k_doc int32 [B, kv_len]."""
     if q.dim() != 4 or k.dim() != 4 or k.shape != v.shape or q.shape[0] != k.shape[0] or q.shape[3] != 128 \
             or k.shape[3] != 128:

@@ -321,3 +321,35 @@ def test_refusals():
                 lambda: model.attention_masked(q, k.expand(1, 8, 2, 128)[:, :1].expand(1, 8, 2, 128), v)):
         with pytest.raises(abi.ZiError):
             bad()
+
+
+@pytest.mark.parametrize("n", [2, 300])
+def test_offsets_past_32_bits(n):
+    """Rows 2^24 elements apart in one buffer: the last ones stand past 2^32 elements (8 GB)."""
+    from stream_diffusion_transformer_b200 import model
+    m, step = 300, 1 << 24
+    q, k, v = inputs(1, n, m, 2, 2, 11)
+    want = check(q, k, v, causal=True)
+    room = torch.empty(m * step, dtype=torch.bfloat16, device="cuda")
+    views = []
+    for i, t in enumerate((q, k, v, want)):
+        views.append(room.as_strided((1, t.shape[1], 2, 128), (m * step, step, 128, 1), (m - t.shape[1]) * step + 256 * i))
+    for view, t in zip(views, (q, k, v, torch.zeros_like(want))):
+        view.copy_(t)
+    model.attention_masked(*views[:3], causal=True, out=views[3])
+    assert torch.equal(views[3], want)
+    for view, t in zip(views, (q, k, v)):
+        assert torch.equal(view, t)
+
+
+@pytest.mark.parametrize("n", [1, 300])
+def test_largest_biases(n):
+    """A slope of 2^20 over 300 places (scores of 2^28.3) leaves each query its own place at any scale: the next key
+    is behind by 2^20, so the result is v of that place, bit for bit."""
+    from stream_diffusion_transformer_b200 import model
+    q, k, v = inputs(1, n, 300, 2, 2, 12)
+    slopes = torch.full((2,), 2.0 ** 20, device="cuda")
+    for scale in (2.0 ** -60, 128 ** -0.5):
+        for softcap in (0.0, 20.0):
+            got = model.attention_masked(q, k, v, scale=scale, softcap=softcap, slopes=slopes)
+            assert torch.equal(got, v[:, 300 - n:])

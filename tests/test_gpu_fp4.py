@@ -191,3 +191,26 @@ def test_empty_and_refusals():
                 lambda: model.gemm_fp4(w, w, out=torch.empty(16, 8, dtype=torch.bfloat16, device="cuda"))):
         with pytest.raises(ValueError):
             bad()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_offsets_past_32_bits(fmt):
+    """More than 2^32 elements going in, and more than 2^31 coming out of a product: the last rows."""
+    from stream_diffusion_transformer_b200 import model
+    rows, cols = 262272, 16384
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    x[-128:] = torch.randn(128, cols, device="cuda")
+    m, tail = model.quantize_fp4(x, fmt), model.quantize_fp4(x[-128:].clone(), fmt)
+    assert torch.equal(m.codes[-128:], tail.codes)
+    assert torch.equal(m.block_scales[-tail.block_scales.numel():], tail.block_scales)
+    if fmt == "nvfp4":
+        assert torch.equal(m.row_scales[-128:], tail.row_scales)
+    x.fill_(1.0)
+    y = model.dequantize_fp4(m)
+    assert torch.equal(y[-128:], model.dequantize_fp4(tail)) and not y[:128].any()
+    del x, y, m
+    a, b = model.quantize_fp4(torch.randn(70000, 64, device="cuda"), fmt), model.quantize_fp4(torch.randn(32768, 64, device="cuda"), fmt)
+    got = model.gemm_fp4(a, b)[-200:].double()
+    da, db = (model.dequantize_fp4(t, torch.float32).double() for t in (a, b))
+    want, size = da[-200:] @ db.t(), da[-200:].abs() @ db.abs().t()
+    assert ((got - want).abs() <= 2.0 ** -8 * want.abs() + 64 * 2.0 ** -23 * size).all()
