@@ -364,37 +364,21 @@ int launch_clustered(int kind, dim3 grid, int threads, uint32_t smem, int cluste
 
 // ---------------------------------------------------------------- 4-bit rows
 
-constexpr int kFp4MaxCols = 16384;
-// From this many rows on the rows alone fill the GPU, and fewer threads per row with more loads on their way each are
-// faster.  Measured with one and four 32-byte spans per thread: 20480 x 3840 bf16 to NVFP4 62.7 / 46.6 us, 4128 x
-// 3840 14.8 / 12.3.
-constexpr int kFp4DeepRows = 1024;
+constexpr int kFp4MaxCols = fp4::kRowsMaxCols;
 constexpr int kMaxDim = 1 << 24;
-
-// A power of two, at least the threads of one scale word.
-int fp4_threads_per_row(int cols) {
-  int tpr = 8;
-  while (tpr < cols / 16 && tpr < fp4::kRowsThreads) tpr *= 2;
-  return tpr;
-}
 
 template <int FMT, typename TIn>
 int run_quantize_fp4(const TIn* x, int rows, int cols, uint8_t* q, uint8_t* bs, float* rs, cudaStream_t st) {
-  const int spans = cols / 16;
-  int tpr = fp4_threads_per_row(cols), nb = (spans + tpr - 1) / tpr;
-  constexpr int kDeep = sizeof(TIn) == 4 ? 2 : 4;
-  static_assert(kFp4MaxCols / 16 <= 4 * fp4::kRowsThreads, "at most 4 spans per thread");
-  while (rows >= kFp4DeepRows && nb < kDeep && tpr > 8) {
-    tpr /= 2;
-    nb = (spans + tpr - 1) / tpr;
-  }
+  const fp4::RowsPlan plan = fp4::rows_plan(rows, cols, int(sizeof(TIn)));
+  const int tpr = plan.tpr;
+  if (tpr * plan.spans < cols / 16) return ZI_ERR_SHAPE;  // columns that no thread takes
   const int per = fp4::kRowsThreads / tpr;
   const int rows_pad = fp4::tiles_down(rows) * 128;
   const int grid = (rows_pad + per - 1) / per;
   prof_pre(st);
-  if (nb <= 1)
+  if (plan.spans == 1)
     fp4::quantize_kernel<FMT, TIn, 1><<<grid, fp4::kRowsThreads, 0, st>>>(x, rows, cols, tpr, q, bs, rs);
-  else if (nb <= 2)
+  else if (plan.spans == 2)
     fp4::quantize_kernel<FMT, TIn, 2><<<grid, fp4::kRowsThreads, 0, st>>>(x, rows, cols, tpr, q, bs, rs);
   else
     fp4::quantize_kernel<FMT, TIn, 4><<<grid, fp4::kRowsThreads, 0, st>>>(x, rows, cols, tpr, q, bs, rs);
@@ -405,7 +389,7 @@ template <int FMT, typename TOut>
 int run_dequantize_fp4(const uint8_t* q, const uint8_t* bs, const float* rs, int rows, int cols, TOut* y,
                        cudaStream_t st) {
   int tpr = fp4::kRowsThreads;  // with many rows, four or more loads on their way per thread
-  while (tpr > 4 && (rows >= kFp4DeepRows ? 4 * tpr > cols / 8 : tpr / 2 >= cols / 8)) tpr /= 2;
+  while (tpr > 4 && (rows >= fp4::kDeepRows ? 4 * tpr > cols / 8 : tpr / 2 >= cols / 8)) tpr /= 2;
   const int per = fp4::kRowsThreads / tpr;
   prof_pre(st);
   fp4::dequantize_kernel<FMT, TOut><<<(rows + per - 1) / per, fp4::kRowsThreads, 0, st>>>(q, bs, rs, rows, cols, tpr, y);
