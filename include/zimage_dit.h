@@ -423,7 +423,8 @@ ZI_API int zi_attention_desc_init(zi_attention_desc* desc);
  * stands at p_i = i + n - q_len, so q_len = 1 is one step over a cache and q_len = n self
  * attention.  The masks given apply together.  A query that sees no key (no keys, all
  * masked, a negative id) gets zeros.  fp32 scores and softmax, probabilities rounded to
- * bf16 for the second product, one rounding of the result.
+ * bf16 for the second product, one rounding of the result; a capped score is off by at most
+ * 2^-17 of the cap and by at most 2^-14 of itself, so a cap far above the scores changes nothing.
  * The scores of keys that are seen, cap and bias included, may be up to 2^29 in size (larger
  * ones are further apart in fp32 than exp2 reaches: their rows may come out as NaN).
  * What key rows past an element's end and rows with a negative id hold is never used (NaN

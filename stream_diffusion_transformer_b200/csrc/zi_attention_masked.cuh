@@ -48,10 +48,14 @@ ZI_DEV float fast_rcp(float x) {
   return y;
 }
 
-// tanh(x) = 1 - 2 / (e^2x + 1): an absolute error of a few 2^-24, which a cap of 50 turns
-// into 10^-5 of a score.  Infinite e^2x gives 1, e^2x = 0 gives -1.
-ZI_DEV float tanh_exp(float x) {
-  return 1.f - 2.f * fast_rcp(fast_exp2(x * 2.885390081777927f) + 1.f);
+// tanh to a relative error of 10^-6 or less, so that scores far below their cap keep their own accuracy.  From 1/4 on
+// 1 - 2 / (e^2x + 1), whose error is a few 2^-24 whatever the result's size (infinite e^2x gives 1, e^2x = 0 gives
+// -1); below it the series up to x^7, whose next term is 62/2835 x^8 < 2^-21 of x.
+ZI_DEV float tanh_score(float x) {
+  const float u = x * x;
+  const float low = x * fmaf(u, fmaf(u, fmaf(u, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f), 1.f);
+  const float high = 1.f - 2.f * fast_rcp(fast_exp2(x * 2.885390081777927f) + 1.f);
+  return fabsf(x) < 0.25f ? low : high;
 }
 
 // ------------------------------------------------------------------ few queries
@@ -217,7 +221,7 @@ __global__ void __launch_bounds__(few::kThreads)
       for (int e = 0; e < 4; ++e) {
         const int h = e >> 1, key = c * kChunk + t * 8 + tid * 2 + (e & 1);
         float y = s[t][e] * p.scale_log2;
-        if (p.cap_log2 != 0.f) y = tanh_exp(y) * p.cap_log2;
+        if (p.cap_log2 != 0.f) y = tanh_score(y) * p.cap_log2;
         if (p.slopes) y -= slope[h] * fabsf(float(pos[h] - key));
         if (part && (key >= lim[h] || (kd && id[t * 2 + (e & 1)] != doc[h]))) y = -INFINITY;
         s[t][e] = y;
@@ -418,7 +422,7 @@ static_assert(kPart + 2 * 32 * 128 * 16 + 256 * 8 <= kBar, "partials fit the rin
 }  // namespace many
 
 // cap tanh(z) for a pair on the FMA pipe, |z| <= 3/4: z P(z^2) with a degree-7 odd polynomial
-// fitted here by the Remez exchange on the absolute error (3.7e-6 at most).  c: its
+// fitted here by the Remez exchange on the absolute error (3.7e-6 at most, and 4.5e-5 of tanh(z)).  c: its
 // coefficients times the cap and the powers of the score's factor, so s2 are raw scores.
 constexpr float kCapRange = 0.75f;
 ZI_DEV uint64_t cap_poly_pair(uint64_t s2, const float* c) {
@@ -877,8 +881,8 @@ __global__ void __launch_bounds__(many::kThreads, 1)
               const float s0 = __uint_as_float(s[2 * c]), s1 = __uint_as_float(s[2 * c + 1]);
               float y0, y1;
               f2_unpack(cap_poly_pair(f2_pack(s0, s1), cc), y0, y1);
-              s[2 * c] = __float_as_uint(near ? y0 : tanh_exp(s0 * p.scale_log2) * p.cap_log2);
-              s[2 * c + 1] = __float_as_uint(near ? y1 : tanh_exp(s1 * p.scale_log2) * p.cap_log2);
+              s[2 * c] = __float_as_uint(near ? y0 : tanh_score(s0 * p.scale_log2) * p.cap_log2);
+              s[2 * c + 1] = __float_as_uint(near ? y1 : tanh_score(s1 * p.scale_log2) * p.cap_log2);
             }
           }
         }
