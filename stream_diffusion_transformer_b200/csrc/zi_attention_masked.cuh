@@ -858,16 +858,38 @@ __global__ void __launch_bounds__(many::kThreads, 1)
         tmem_wait_ld();
 #pragma unroll
         for (int c = 0; c < 4; ++c) reg_fence32(&s[c * 32]);
+        // bit c of vis: the row sees key j 128 + c
+        uint32_t vis[4];
+        auto see = [&]() {
+          const int left = lim - j * 128;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) vis[w] = left >= 32 * w + 32 ? ~0u : left <= 32 * w ? 0u : (1u << (left - 32 * w)) - 1u;
+        };
+        if constexpr (DOC) {
+          if (part) {
+            see();
+            for (uint32_t todo = ~0u; todo;) {  // once for each document among the warp's rows
+              const int d = __shfl_sync(0xffffffffu, doc, __ffs(todo) - 1);
+              todo &= ~__ballot_sync(0xffffffffu, doc == d);
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                const uint32_t same = __ballot_sync(0xffffffffu, id[w] == d);
+                if (doc == d) vis[w] &= same;
+              }
+            }
+          }
+        }
         if constexpr (CAP) {
-          // |z| within the polynomial's range over the row's keys, or (scores near the cap and past it) through
-          // exp and a reciprocal.  A NaN, of a key row that nobody sees, stays in its column and is masked below.
+          // |z| within the polynomial's range over the keys that the row sees, or (scores near the cap and past it)
+          // through exp and a reciprocal; each row by its own keys alone, whatever its neighbours and hidden keys hold.
+          // A NaN, of a key row that nobody sees, stays in its column and is masked below.
           float mx4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int c = 0; c < 128; c += 2)
             mx4[c / 2 & 3] = max3f(mx4[c / 2 & 3], fabsf(__uint_as_float(s[c])), fabsf(__uint_as_float(s[c + 1])));
-          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-          const bool near = p.cap_poly && mx * p.scale_log2 <= kCapRange;
-          if (__all_sync(0xffffffffu, near)) {
+          float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+          bool near = p.cap_poly && mx * p.scale_log2 <= kCapRange;
+          auto poly = [&]() {
 #pragma unroll
             for (int c = 0; c < 64; ++c) {
               float y0, y1;
@@ -875,15 +897,26 @@ __global__ void __launch_bounds__(many::kThreads, 1)
               s[2 * c] = __float_as_uint(y0);
               s[2 * c + 1] = __float_as_uint(y1);
             }
-          } else {  // some row of the warp needs the other way; each takes its own, whatever its neighbours hold
+          };
+          if (__builtin_expect(__all_sync(0xffffffffu, near), 1)) {
+            poly();
+          } else {
+            if (part && p.cap_poly && !near) {  // perhaps by hidden keys alone
+              if constexpr (!DOC) see();
+              mx = 0.f;
 #pragma unroll
-            for (int c = 0; c < 64; ++c) {
-              const float s0 = __uint_as_float(s[2 * c]), s1 = __uint_as_float(s[2 * c + 1]);
-              float y0, y1;
-              f2_unpack(cap_poly_pair(f2_pack(s0, s1), cc), y0, y1);
-              s[2 * c] = __float_as_uint(near ? y0 : tanh_score(s0 * p.scale_log2) * p.cap_log2);
-              s[2 * c + 1] = __float_as_uint(near ? y1 : tanh_score(s1 * p.scale_log2) * p.cap_log2);
+              for (int c = 0; c < 128; ++c)
+                if (vis[c >> 5] >> (c & 31) & 1u) mx = fmaxf(mx, fabsf(__uint_as_float(s[c])));
+              near = mx * p.scale_log2 <= kCapRange;
             }
+            if (near) {
+              poly();
+            } else {
+#pragma unroll
+              for (int c = 0; c < 128; ++c)
+                s[c] = __float_as_uint(tanh_score(__uint_as_float(s[c]) * p.scale_log2) * p.cap_log2);
+            }
+            __syncwarp();
           }
         }
         float base = 0.f;  // what every score of the row in this tile still lacks, in the exp2 domain
@@ -903,22 +936,7 @@ __global__ void __launch_bounds__(many::kThreads, 1)
           }
         }
         if (part) {
-          // bit c of vis: the row sees key j 128 + c
-          uint32_t vis[4];
-          const int left = lim - j * 128;
-#pragma unroll
-          for (int w = 0; w < 4; ++w) vis[w] = left >= 32 * w + 32 ? ~0u : left <= 32 * w ? 0u : (1u << (left - 32 * w)) - 1u;
-          if constexpr (DOC) {
-            for (uint32_t todo = ~0u; todo;) {  // once for each document among the warp's rows
-              const int d = __shfl_sync(0xffffffffu, doc, __ffs(todo) - 1);
-              todo &= ~__ballot_sync(0xffffffffu, doc == d);
-#pragma unroll
-              for (int w = 0; w < 4; ++w) {
-                const uint32_t same = __ballot_sync(0xffffffffu, id[w] == d);
-                if (doc == d) vis[w] &= same;
-              }
-            }
-          }
+          if constexpr (!DOC) see();
 #pragma unroll
           for (int c = 0; c < 128; ++c)
             if (!(vis[c >> 5] >> (c & 31) & 1u)) s[c] = __float_as_uint(-INFINITY);

@@ -61,3 +61,30 @@ def test_caps_of_any_size(cap, n, m, H, Hk):
         if cap >= 1e5:  # scores of 20 at most: tanh takes (20 / cap)^2 / 3 < 2^-26 of them
             free, tol0 = causal_formula(q, k, v, 2.0 ** 200, slopes)
             assert ((got - free).abs() <= tol0).all()
+
+
+@pytest.mark.parametrize("slope", [False, True])
+@pytest.mark.parametrize("n,m", [(2, 400), (300, 400)])
+def test_hidden_keys_leave_a_capped_row_as_it_is(n, m, slope):
+    """Bit for bit: keys past the end, later ones and those of other documents, however large their scores are."""
+    from stream_diffusion_transformer_b200 import model
+    q, k, v = inputs(1, n, m, 2, 1, 21)
+    kw = dict(softcap=30.0, slopes=slopes_of(2) if slope else None)
+
+    def with_loud(rows, by):
+        k2, v2 = k.clone(), v.clone()
+        k2[:, rows], v2[:, rows] = k2[:, rows] * by, v2[:, rows] * 100.0
+        return k2, v2
+    used = m - 70
+    for by in (50.0, 2.0 ** 120, float("nan")):
+        a = model.attention_masked(q, k, v, kv_len=i32(used), **kw)
+        assert torch.equal(model.attention_masked(q, *with_loud(slice(used, m), by), kv_len=i32(used), **kw), a)
+    a = model.attention_masked(q, k, v, causal=True, **kw)
+    for last in (m - n, m - 1 - n // 2):  # the keys behind the one at place `last`
+        got = model.attention_masked(q, *with_loud(slice(last + 1, m), 50.0), causal=True, **kw)
+        seen = last - (m - n) + 1  # queries that stand at `last` or before
+        assert torch.equal(got[:, :seen], a[:, :seen]) and not torch.equal(got, a)
+    ids = (torch.arange(m, dtype=torch.int32, device="cuda") % 3)[None].contiguous()
+    own = torch.full((1, n), 1, dtype=torch.int32, device="cuda")
+    a = model.attention_masked(q, k, v, q_doc=own, k_doc=ids, **kw)
+    assert torch.equal(model.attention_masked(q, *with_loud(ids[0] != 1, 50.0), q_doc=own, k_doc=ids, **kw), a)
