@@ -470,7 +470,9 @@ ZI_API int zi_dequantize_fp4(int format, const uint8_t* d_q, const uint8_t* d_bs
 
 /* C[M, N] = bf16( ra[m] rb[n] sum_k A[m, k] B[n, k] ), A and B 4-bit matrices of one format
  * (codes, block scales, and row scales for NVFP4; NULL row scales for MXFP4), on the
- * tensor cores (kind::mxf4nvf4), fp32 accumulate, one rounding.  A row that holds a NaN
+ * tensor cores (kind::mxf4nvf4), fp32 accumulate, one rounding; right wherever the result is
+ * one of bf16's normal numbers, zero or past the largest, however small or large ra[m] and
+ * rb[n] are.  A row that holds a NaN
  * scale gives a row (of A) or column (of B) of NaN.
  * K % 32 == 0, N % 8 == 0, M >= 0 (0 enqueues nothing), each at most 2^24 (ZI_ERR_SHAPE); 16-byte
  * aligned pointers.  No workspace, nothing kept between calls. */
