@@ -467,7 +467,8 @@ struct GemmParams {
 };
 
 // ------------------------------------------------------------------ product: few rows
-// One CTA per 128 rows of B (output columns) x TN rows of A, with B as the instruction's
+// One CTA per 128 rows of B (output columns) x TN rows of A (one tile of 16, 32 or 64 rows, or any number of 128: a tile's
+// block scales start where a scale tile of 128 rows does), with B as the instruction's
 // M operand: a call with few rows is bound by reading B, so B's rows fill the tensor core
 // and A's few rows are its N.  A cluster of CTAs shares a tile's K: each takes a run of
 // stages, leaves its fp32 partial in its own smem, and sums a part of the tile over the
@@ -580,13 +581,12 @@ __global__ void __launch_bounds__(kNarrowThreads)
           copy_scales(tsb + 4 * t, sc_addr + t * kTileBytes);
           copy_scales(tsa + 4 * t, sc_addr + L::kSc + t * kTileBytes);
         }
-        const uint32_t a_col = uint32_t(m0 & 127) / 32;  // the tile's rows inside its 128-row scale tile
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           if (k < ksteps) {
             const int t = FMT == MX ? k >> 1 : k;
             mma<FMT>(tmem, smem_desc_sw128(b_addr + k * 32, 16), smem_desc_sw128(a_addr + k * 32, 16),
-                     idesc<FMT>(128, TN, FMT == MX ? k & 1 : 0), tsb + 4 * t, tsa + 4 * t + a_col,
+                     idesc<FMT>(128, TN, FMT == MX ? k & 1 : 0), tsb + 4 * t, tsa + 4 * t,
                      (it | k) != 0 ? 1u : 0u);
           }
         }

@@ -398,6 +398,7 @@ int run_dequantize_fp4(const uint8_t* q, const uint8_t* bs, const float* rs, int
 
 // ---------------------------------------------------------------- 4-bit product
 
+// TN below 128: calls of at most TN rows (one row tile).
 template <int FMT, int TN>
 int run_fp4_narrow(DevInfo* dev, const uint8_t* a, const uint8_t* b, const fp4::GemmParams& p, cudaStream_t st) {
   using L = fp4::NarrowSmem<FMT, TN>;
