@@ -565,7 +565,8 @@ def attention_masked(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, scale
     q bf16 [B, q_len, H, 128], k and v bf16 [B, kv_len, Hk, 128] with H a multiple of Hk, in any
     strides with contiguous heads (multiples of 8, no broadcast dimensions); returns bf16
     [B, q_len, H, 128].  softcap 0 = none; slopes fp32 [H];
-    prefix_len (with causal) and kv_len int32 [B]; q_doc int32 [B, q_len] with k_doc int32 [B, kv_len]."""
+    prefix_len (with causal) and kv_len int32 [B]; q_doc int32 [B, q_len] with k_doc int32 [B, kv_len].
+    No element or no query gives an empty result, no key rows zeros."""
     if q.dim() != 4 or k.dim() != 4 or k.shape != v.shape or q.shape[0] != k.shape[0] or q.shape[3] != 128 \
             or k.shape[3] != 128:
         raise ValueError("attention_masked: q [B, q_len, H, 128] and k, v [B, kv_len, Hk, 128] are needed")
@@ -594,6 +595,8 @@ def attention_masked(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, scale
                             1 if causal else 0, small("prefix_len", prefix_len, torch.int32, B),
                             small("kv_len", kv_len, torch.int32, B), small("q_doc", q_doc, torch.int32, B, n),
                             small("k_doc", k_doc, torch.int32, B, m))
+    if B == 0 or n == 0 or m == 0:
+        return out.zero_()
     _launch(device, "zi_attention_masked", ctypes.byref(d))
     return out
 
