@@ -122,8 +122,8 @@ typedef struct zi_block_weights {
   const float* s_out;      /* [D] */
   const uint8_t* w2_8;     /* [D, Fp] e4m3 codes of w2 (zero columns F..Fp) */
   const float* s_2;        /* [D] */
-  /* Optional 4-bit projections (zi_quantize_fp4 of the same matrices; not beside e4m3
-   * ones): codes, block scales and, for NVFP4, row scales (all row scales NULL means
+  /* Optional 4-bit projections (zi_quantize_fp4 of the same matrices, which are not read then
+   * but have to be given all the same; not beside e4m3 ones): codes, block scales and, for NVFP4, row scales (all row scales NULL means
    * MXFP4).  QKV and w1|w3 (or none), then optionally the output projection and w2 too.
    * The rows going into each are brought to 4 bits by a pass before it; the products run
    * on the tensor cores in kind::mxf4nvf4 with the same fused epilogues.  Blocks in 4 bits
@@ -428,8 +428,9 @@ ZI_API int zi_attention_desc_init(zi_attention_desc* desc);
  * The scores of keys that are seen, cap and bias included, may be up to 2^29 in size (larger
  * ones are further apart in fp32 than exp2 reaches: their rows may come out as NaN).
  * What key rows past an element's end and rows with a negative id hold is never used (NaN
- * included).  A key that some queries see has to be finite: the product of a masked
- * probability (zero) and a NaN or infinity in a seen row of v is NaN.
+ * included).  Every other key row has to be finite, those that no query sees by its order or
+ * by the ids given among them (an id that no query has): the product of a masked probability
+ * (zero) and a NaN or infinity in v is NaN.
  * No workspace, nothing kept between calls: any number of calls may run at once. */
 ZI_API int zi_attention_masked(const zi_attention_desc* desc, zi_stream_t stream);
 
@@ -470,10 +471,10 @@ ZI_API int zi_dequantize_fp4(int format, const uint8_t* d_q, const uint8_t* d_bs
 
 /* C[M, N] = bf16( ra[m] rb[n] sum_k A[m, k] B[n, k] ), A and B 4-bit matrices of one format
  * (codes, block scales, and row scales for NVFP4; NULL row scales for MXFP4), on the
- * tensor cores (kind::mxf4nvf4), fp32 accumulate, one rounding; right wherever the result is
- * one of bf16's normal numbers, zero or past the largest, however small or large ra[m] and
- * rb[n] are.  A row that holds a NaN
- * scale gives a row (of A) or column (of B) of NaN.
+ * tensor cores (kind::mxf4nvf4), fp32 accumulate, one rounding.  Where the sum over k is in
+ * fp32's range on the way, the result is right wherever it is one of bf16's normal numbers,
+ * zero or past the largest, however small or large ra[m] and rb[n] are.  A row that holds a
+ * NaN scale gives a row (of A) or column (of B) of NaN.
  * K % 32 == 0, N % 8 == 0, M >= 0 (0 enqueues nothing), each at most 2^24 (ZI_ERR_SHAPE); 16-byte
  * aligned pointers.  No workspace, nothing kept between calls. */
 ZI_API int zi_gemm_fp4(int format, const uint8_t* d_a, const uint8_t* d_abs, const float* d_ars, const uint8_t* d_b,
