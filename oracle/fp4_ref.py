@@ -124,6 +124,35 @@ def block_forward(x, W, prefix, d, angles, c=None, fmt="nvfp4", all=False):
     return x1 + gate_mlp * ref.rms_norm(f, W(f"{prefix}.ffn_norm2.weight"))
 
 
+def block_forward_rows(x, W, prefix, d, angles, c, rows, fmt="nvfp4", all=False):
+    """block_forward(x, ...)[rows] for the selected query rows only (keys and values from every row): every step but
+    attention is per row, and so are the 4-bit formats.  ffn has to be a multiple of 32 (no padded columns)."""
+    from . import zimage_ref as ref
+
+    def lin(h, w, four=True):
+        return fp4_linear(to_bf16(h), w, fmt) if four else ref.linear(h, w)
+
+    S, D = x.shape
+    n = len(rows)
+    if c is not None:
+        scale_msa, gate_msa, scale_mlp, gate_mlp = ref.adaln(c, W, prefix)
+    else:
+        scale_msa = scale_mlp = 0.0
+        gate_msa = gate_mlp = 1.0
+    a, ff = f"{prefix}.attention", f"{prefix}.feed_forward"
+    h = ref.rms_norm(x, W(f"{prefix}.attention_norm1.weight")) * (1.0 + scale_msa)
+    q = lin(h[rows], W(f"{a}.to_q.weight")).reshape(n, d.heads, d.head_dim)
+    k, v = (lin(h, W(f"{a}.{nm}.weight")).reshape(S, d.heads, d.head_dim) for nm in ("to_k", "to_v"))
+    q = ref.apply_rope(ref.rms_norm(q, W(f"{a}.norm_q.weight")), angles[rows])
+    k = ref.apply_rope(ref.rms_norm(k, W(f"{a}.norm_k.weight")), angles)
+    o = lin(ref.attention(q, k, v).reshape(n, D), W(f"{a}.to_out.weight"), all)
+    x1 = x[rows] + gate_msa * ref.rms_norm(o, W(f"{prefix}.attention_norm2.weight"))
+    h2 = ref.rms_norm(x1, W(f"{prefix}.ffn_norm1.weight")) * (1.0 + scale_mlp)
+    u = ref.silu(lin(h2, W(f"{ff}.w1.weight"))) * lin(h2, W(f"{ff}.w3.weight"))
+    f = lin(u, W(f"{ff}.w2.weight"), all)
+    return x1 + gate_mlp * ref.rms_norm(f, W(f"{prefix}.ffn_norm2.weight"))
+
+
 def to_bf16(x):
     """x rounded to bf16 (nearest even), as fp64."""
     u = np.asarray(x, dtype=np.float32).view(np.uint32)
