@@ -49,23 +49,24 @@ constexpr int kRowsMaxCols = 16384;  // four spans of 16 columns on each thread 
 constexpr int kDeepRows = 1024;
 
 // How quantize_kernel takes rows of `cols` columns: threads per row, a power of two that is at least the threads of one
-// scale word, and spans per thread as compiled (1, 2 or 4).  tpr * spans >= cols / 16.
+// scale word, and spans per thread (1 to kMaxSpans, each compiled).  tpr * spans >= cols / 16.
 struct RowsPlan {
   int tpr, spans;
 };
+constexpr int kMaxSpans = 4;
 __host__ inline RowsPlan rows_plan(int rows, int cols, int bytes) {
   const int all = cols / 16;
   auto each = [&](int tpr) { return (all + tpr - 1) / tpr; };
   int tpr = 8;
   while (tpr < all && tpr < kRowsThreads) tpr *= 2;
-  // fp32 spans are twice as long: two of them are as many loads.  Three spans a thread (run as four) may become five or
-  // six with half the threads, which no compiled count covers
+  // fp32 spans are twice as long: two of them are as many loads.  Three spans become five or six with half the threads;
+  // those counts, compiled too, were slower up to 4,128 rows or up to 8% faster past that (1024 x 1536 bf16 to NVFP4 4.0
+  // against 3.1 us, 20480 x 10240 100 against 108), and three run as four took 4128 x 10240 from 25.3 to 27.8
   const int deep = bytes == 4 ? 2 : 4;
-  while (rows >= kDeepRows && each(tpr) < deep && tpr > 8 && each(tpr / 2) <= 4) tpr /= 2;
-  const int n = each(tpr);
-  return {tpr, n <= 1 ? 1 : n <= 2 ? 2 : 4};
+  while (rows >= kDeepRows && each(tpr) < deep && tpr > 8 && each(tpr / 2) <= kMaxSpans) tpr /= 2;
+  return {tpr, each(tpr)};
 }
-static_assert(kRowsMaxCols / 16 <= 4 * kRowsThreads, "at most 4 spans per thread");
+static_assert(kRowsMaxCols / 16 <= kMaxSpans * kRowsThreads, "spans per thread");
 
 // 16 consecutive elements of a row, as loaded.
 template <typename TIn>

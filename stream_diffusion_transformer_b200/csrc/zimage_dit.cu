@@ -371,17 +371,20 @@ template <int FMT, typename TIn>
 int run_quantize_fp4(const TIn* x, int rows, int cols, uint8_t* q, uint8_t* bs, float* rs, cudaStream_t st) {
   const fp4::RowsPlan plan = fp4::rows_plan(rows, cols, int(sizeof(TIn)));
   const int tpr = plan.tpr;
-  if (tpr * plan.spans < cols / 16) return ZI_ERR_SHAPE;  // columns that no thread takes
+  if (plan.spans > fp4::kMaxSpans) return ZI_ERR_SHAPE;  // columns that no thread takes
   const int per = fp4::kRowsThreads / tpr;
   const int rows_pad = fp4::tiles_down(rows) * 128;
   const int grid = (rows_pad + per - 1) / per;
+  auto run = [&](auto spans) {
+    fp4::quantize_kernel<FMT, TIn, decltype(spans)::value><<<grid, fp4::kRowsThreads, 0, st>>>(x, rows, cols, tpr, q, bs, rs);
+  };
   prof_pre(st);
-  if (plan.spans == 1)
-    fp4::quantize_kernel<FMT, TIn, 1><<<grid, fp4::kRowsThreads, 0, st>>>(x, rows, cols, tpr, q, bs, rs);
-  else if (plan.spans == 2)
-    fp4::quantize_kernel<FMT, TIn, 2><<<grid, fp4::kRowsThreads, 0, st>>>(x, rows, cols, tpr, q, bs, rs);
-  else
-    fp4::quantize_kernel<FMT, TIn, 4><<<grid, fp4::kRowsThreads, 0, st>>>(x, rows, cols, tpr, q, bs, rs);
+  switch (plan.spans) {
+    case 1: run(std::integral_constant<int, 1>{}); break;
+    case 2: run(std::integral_constant<int, 2>{}); break;
+    case 3: run(std::integral_constant<int, 3>{}); break;
+    default: run(std::integral_constant<int, 4>{}); break;
+  }
   return launched(ZI_KERNEL_QUANTIZE_FP4, st);
 }
 

@@ -19,7 +19,7 @@ int main() {
           for (int k = 0; k < p.spans; ++k)  // as quantize_kernel walks them
             if (sub + k * p.tpr < cols / 16) ++taken[size_t(sub + k * p.tpr)];
         bool ok = p.tpr >= 8 && p.tpr <= kRowsThreads && (p.tpr & (p.tpr - 1)) == 0 &&
-                  (p.spans == 1 || p.spans == 2 || p.spans == 4);
+                  p.spans >= 1 && p.spans <= kMaxSpans;
         for (int n : taken) ok = ok && n == 1;
         if (!ok && ++failures <= 20)
           std::printf("FAIL rows %d cols %d bytes %d: %d threads x %d spans\n", rows, cols, bytes, p.tpr, p.spans);
