@@ -65,8 +65,8 @@ ZI_DEV float tanh_score(float x) {
 // keys through a private smem ring with TMA (3 chunks of K and V deep, 24 KB per warp, two
 // CTAs per SM), takes scores and products with mma.sync m16n8k16 (16 rows padded: the tensor
 // work is small beside the loads) and keeps its own running maximum and sum.  The warps' and
-// then the cluster's partials are joined in a fixed order.  One query over 2 x 16,896 keys, 30 heads: 79.8 us,
-// 5.7 TB/s.
+// then the cluster's partials are joined in a fixed order.  One query over 2 x 16,896 keys, 30 heads: 80.9 us,
+// 5.6 TB/s.
 namespace few {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
@@ -398,8 +398,8 @@ __global__ void __launch_bounds__(few::kThreads)
 //   smem before the product: zero probabilities times NaN would be NaN;
 // - with few CTAs, a cluster that shares a unit's keys and joins its partials through
 //   distributed shared memory in rank order (no workspace, no atomics).
-// Bound by the softmax's latency between a tile's two products: 16,896 tokens x 30 heads with cap and bias 5.68 ms
-// (772 TFLOP/s; 3.1 us a step of 256 x 128 scores against 1.1 of MMA); a pack of 4224 in five documents 166 us.
+// Bound by the softmax's latency between a tile's two products: 16,896 tokens x 30 heads with cap and bias 5.76 ms
+// (760 TFLOP/s; 3.1 us a step of 256 x 128 scores against 1.1 of MMA); a pack of 4224 in five documents 167 us.
 // Warps 0..3 rows of tile A, 4..7 of tile B, 8 K loads, 9 MMA, 10 V loads, 11 clears V.
 namespace many {
 constexpr int kThreads = 384;

@@ -255,8 +255,8 @@ ZI_DEV void nv_units(float* v, float sc, uint32_t row_exp) {
 // thread i % tpr.  x is read once, all of a thread's spans at once, and an NVFP4 row waits
 // in registers, as it was loaded, for its maximum.  Rows past the end up to the scale tile's
 // 128 only write their zero scales.
-// Bound by HBM for MXFP4 (20480 x 3840 bf16 32.5 us, 6.1 TB/s), by issue slots for NVFP4, whose rows wait for their
-// maximum and whose ties are exact (same rows 40.7 us, 5.0 TB/s; 4128 x 3840 11.3 us).
+// Bound by HBM for MXFP4 (20480 x 3840 bf16 32.2 us, 6.1 TB/s), by issue slots for NVFP4, whose rows wait for their
+// maximum and whose ties are exact (same rows 40.5 us, 5.0 TB/s; 4128 x 3840 11.8 us, 4128 x 10240 24.6 us).
 template <int FMT, typename TIn, int NB>
 __global__ void __launch_bounds__(kRowsThreads) quantize_kernel(const TIn* __restrict__ x, int rows, int cols, int tpr,
                                                                uint8_t* __restrict__ q, uint8_t* __restrict__ bs,
@@ -474,8 +474,9 @@ struct GemmParams {
 // and A's few rows are its N.  A cluster of CTAs shares a tile's K: each takes a run of
 // stages, leaves its fp32 partial in its own smem, and sums a part of the tile over the
 // cluster's CTAs in rank order.  Warps: 0 loads, 1 MMA, 2..5 epilogue.
-// About 6 us are fixed (launch, filling the ring, the join): 1 x 3840 x 3840 NVFP4 7.7 us against 1.3 of reading B,
-// 77 x 11520 x 3840 MXFP4 15.2 us against 3.9.
+// About 6 us are fixed (launch, filling the ring, the join): 1 x 3840 x 3840 NVFP4 7.9 us against 1.3 of reading B.
+// 77 x 11520 x 3840 MXFP4 14.7 us against 3.9: 90 tiles in clusters of two are 180 CTAs, so that 32 SMs hold two and the
+// others one, and 77 rows run as 128.
 constexpr int kNarrowThreads = 192;
 
 template <int FMT, int TN>
@@ -674,14 +675,14 @@ __global__ void __launch_bounds__(kNarrowThreads)
 // M = 256 MMAs for both SMs.
 // - Scales reach TMEM through registers: four warps, one per lane quarter, read a stage's
 //   scale tiles from smem and store them with tcgen05.st while earlier MMAs run.  tcgen05.cp
-//   would do it in the tensor core's own queue, where each 512-byte tile took about 55 cycles
-//   between the MMAs (4128 x 20480 x 3840 NVFP4: 252 us with it).
+//   would do it in the tensor core's own queue, between the MMAs (4128 x 20480 x 3840 NVFP4:
+//   252 us with it, 174 without when that was changed).
 // - TMEM holds one accumulator (256 columns) and one scale buffer per smem stage; there is no
 //   room for a second accumulator, so the epilogue warps take the whole accumulator into
 //   registers (128 columns each) and hand it back before they scale and store: the MMAs of
 //   the next tile wait for the TMEM reads alone.
-// 4128 x 20480 x 3840: NVFP4 156 us (4.15 PFLOP/s), MXFP4 143 us (4.5).  Bound by the MMA sequence: copies without
-// operand loads, without scales and without stores took 152, 144 and 151 us (NVFP4), without all three 141.
+// 4128 x 20480 x 3840: NVFP4 162 us (4.0 PFLOP/s), MXFP4 146 us (4.4).  What bounds it is not settled: the tensor pipe is
+// active 54% of the time, issue slots 25%, DRAM 12%.
 // Warps: 0 loads, 1 MMA, 2..3 idle, 4..7 scales, 8..15 epilogue; registers move from the
 // first two warpgroups to the epilogue (128 a thread at launch; 56 + 64 + 2 x 192 = 504 <= 512).
 constexpr int kWideThreads = 512;
